@@ -117,6 +117,20 @@ _SIGS = {
                                   _P, _P, _P, _P, _P, _P, _SZ, _P]),
 }
 
+# include/usaf_train.h: auxiliary router losses, dense router gradient products, 8-bit activations
+_TRAIN_SIGS = {
+    "usaf_router_aux_workspace_size": (_SZ, [_I64, _I64, _I64, _I64]),
+    "usaf_router_aux_fwd": (_INT, [_I64, _I64, _I64, _P, _I64, _P, _P, _P, _I64, _D, _D, _P, _P,
+                                   _P, _P, _P, _P, _SZ, _P]),
+    "usaf_router_aux_bwd": (_INT, [_I64, _I64, _I64, _P, _I64, _P, _P, _I64, _D, _D, _P, _P, _P,
+                                   _P, _I64, _INT, _P, _P]),
+    "usaf_router_grad_workspace_size": (_SZ, [_I64, _I64, _I64, _INT]),
+    "usaf_router_grad": (_INT, [_I64, _I64, _I64, _INT, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P,
+                                _SZ, _P]),
+    "usaf_act8_save": (_INT, [_P, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "usaf_act8_restore": (_INT, [_P, _INT, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+}
+
 
 def header_symbols() -> list:
     """Names of the functions include/usaf.h declares."""
@@ -136,7 +150,7 @@ def lib():
         if not os.path.exists(path):
             _build.build()
         L = ctypes.CDLL(path)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in (*_SIGS.items(), *_TRAIN_SIGS.items()):
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
@@ -511,6 +525,172 @@ def reselect_carry(new_idx, old_idx, p_in, m_in, v_in, w_seg0, n_seg0, w_seg1, p
         old_idx.numel(), _ptr(p_in), _ptr(m_in), _ptr(v_in), _ptr(w_seg0), int(n_seg0),
         _ptr(w_seg1), _dt(w_seg0), _ptr(p_out), _ptr(m_out), _ptr(v_out), _ptr(n_kept),
         _ptr(dev_status), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- usaf_train.h
+ACT8_BLOCK = 16
+
+
+def _check_t(name: str, t, dtype, shape, device, optional=False, strided=False) -> None:
+    """The library reads and writes bare pointers: refuse a tensor of another dtype, shape, layout
+    or device before any launch. strided: the last axis contiguous, rows any distance apart."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {list(shape)} {dtype}, got {list(t.shape)} {t.dtype}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: expected a tensor on the same CUDA device, got {t.device}")
+    if strided:
+        if t.shape[0] and (t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name}: rows must be contiguous and not overlap")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _ld(t) -> int:
+    """Distance between the rows of a [rows, n] tensor in elements (torch keeps any stride for one
+    row)."""
+    return max(int(t.stride(0)), t.shape[1])
+
+
+def router_aux_workspace_size(T: int, E: int, k: int, G: int = 1) -> int:
+    return int(lib().usaf_router_aux_workspace_size(int(T), int(E), int(k), int(G)))
+
+
+def router_aux_fwd(logits, topk_idx, k, count, prob_sum, n_tok, loss, coef_balance, coef_z,
+                   token_mask=None, group_offset=None, dev_status=None, ws=None, stream=None):
+    """usaf_router_aux_fwd: balance loss, z-loss and per-expert counts of logits [T,E] (rows may be
+    a stride apart); count and prob_sum [G,E], n_tok [G], loss [3] = (total, balance, z)."""
+    T, E = logits.shape
+    G, d = count.shape[0], logits.device
+    _check_t("logits", logits, torch.float32, (T, E), d, strided=True)
+    _check_t("topk_idx", topk_idx.reshape(-1), torch.int32, (T * k,), d)
+    _check_t("count", count, torch.int32, (G, E), d)
+    _check_t("prob_sum", prob_sum, torch.float32, (G, E), d)
+    _check_t("n_tok", n_tok, torch.int32, (G,), d)
+    _check_t("loss", loss, torch.float32, (3,), d)
+    _check_t("token_mask", token_mask, torch.uint8, (T,), d, optional=True)
+    _check_t("group_offset", group_offset, torch.int32, (G + 1,), d, optional=G == 1)
+    if ws is None:
+        ws = _ws(router_aux_workspace_size(T, E, k, G), d)
+    _check("usaf_router_aux_fwd", lib().usaf_router_aux_fwd(
+        T, E, int(k), _ptr(logits), _ld(logits), _ptr(topk_idx), _ptr(token_mask),
+        _ptr(group_offset), G, float(coef_balance), float(coef_z), _ptr(count), _ptr(prob_sum),
+        _ptr(n_tok), _ptr(loss), _ptr(dev_status), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def router_aux_bwd(logits, k, count, n_tok, dlogit, coef_balance, coef_z, d_loss=None,
+                   token_mask=None, group_offset=None, accumulate=0, dev_status=None,
+                   stream=None):
+    """usaf_router_aux_bwd: the gradient of the forward's loss[0] times d_loss ([1], None: 1) into
+    dlogit [T,E] (accumulate = 1 adds); count and n_tok as the forward wrote them."""
+    T, E = logits.shape
+    G, d = count.shape[0], logits.device
+    _check_t("logits", logits, torch.float32, (T, E), d, strided=True)
+    _check_t("dlogit", dlogit, torch.float32, (T, E), d, strided=True)
+    _check_t("count", count, torch.int32, (G, E), d)
+    _check_t("n_tok", n_tok, torch.int32, (G,), d)
+    _check_t("d_loss", d_loss, torch.float32, (1,), d, optional=True)
+    _check_t("token_mask", token_mask, torch.uint8, (T,), d, optional=True)
+    _check_t("group_offset", group_offset, torch.int32, (G + 1,), d, optional=G == 1)
+    _check("usaf_router_aux_bwd", lib().usaf_router_aux_bwd(
+        T, E, int(k), _ptr(logits), _ld(logits), _ptr(token_mask), _ptr(group_offset), G,
+        float(coef_balance), float(coef_z), _ptr(count), _ptr(n_tok), _ptr(d_loss), _ptr(dlogit),
+        _ld(dlogit), int(accumulate), _ptr(dev_status), _stream(stream)))
+
+
+def router_grad_workspace_size(T: int, E: int, H: int, dtype) -> int:
+    """dtype: torch.bfloat16 or torch.float32, of x and dx."""
+    dt = BF16 if dtype == torch.bfloat16 else F32
+    return int(lib().usaf_router_grad_workspace_size(int(T), int(E), int(H), dt))
+
+
+def router_grad(dlogit, x, w_router, g_router=None, g_in=None, dx=None, dx_in=None,
+                dev_status=None, ws=None, stream=None):
+    """usaf_router_grad: g_router = g_in + dlogit^T x and dx = dx_in + dlogit w_router, each only
+    where its output is given (g_in / dx_in None: zero; they may be the outputs themselves)."""
+    T, E = dlogit.shape
+    ref = x if x is not None else dx
+    if ref is None:
+        raise ValueError("x is required")
+    H, d = ref.shape[1], dlogit.device
+    _check_t("dlogit", dlogit, torch.float32, (T, E), d, strided=True)
+    _check_t("x", x, ref.dtype, (T, H), d, optional=g_router is None)
+    _check_t("w_router", w_router, torch.float32, (E, H), d, optional=dx is None)
+    for name, t in (("g_router", g_router), ("g_in", g_in)):
+        _check_t(name, t, torch.float32, (E, H), d, optional=True)
+    for name, t in (("dx", dx), ("dx_in", dx_in)):
+        _check_t(name, t, ref.dtype, (T, H), d, optional=True)
+    if ws is None:
+        ws = _ws(router_grad_workspace_size(T, E, H, ref.dtype), d)
+    _check("usaf_router_grad", lib().usaf_router_grad(
+        T, E, H, _dt(ref), _ptr(dlogit), _ld(dlogit), _ptr(x), _ptr(w_router), _ptr(g_in),
+        _ptr(g_router), _ptr(dx_in), _ptr(dx), _ptr(dev_status), _ptr(ws), ws.numel(),
+        _stream(stream)))
+
+
+@dataclass
+class ActStore8:
+    """A layer's x and h between its forward and its backward, as 8-bit codes with one exponent
+    byte per 16 values (the format is in include/usaf_train.h)."""
+    x_code: torch.Tensor
+    x_exp: torch.Tensor
+    h_code: torch.Tensor
+    h_exp: torch.Tensor
+
+    @staticmethod
+    def shapes(s: Shape) -> tuple:
+        cap = routed_rows_capacity(s)
+        return ((s.T, s.H), (s.T, -(-s.H // ACT8_BLOCK)), (2 * s.I, cap),
+                (2 * s.I, cap // ACT8_BLOCK))
+
+    @staticmethod
+    def empty(s: Shape, device="cuda") -> "ActStore8":
+        dts = (torch.int8, torch.uint8, torch.int8, torch.uint8)
+        return ActStore8(*[torch.empty(sh, dtype=dt, device=device)
+                           for sh, dt in zip(ActStore8.shapes(s), dts)])
+
+    def nbytes(self) -> int:
+        return sum(t.numel() for t in (self.x_code, self.x_exp, self.h_code, self.h_exp))
+
+    def check(self, s: Shape, device) -> None:
+        sh = ActStore8.shapes(s)
+        _check_t("x_code", self.x_code, torch.int8, sh[0], device)
+        _check_t("x_exp", self.x_exp, torch.uint8, sh[1], device)
+        _check_t("h_code", self.h_code, torch.int8, sh[2], device)
+        _check_t("h_exp", self.h_exp, torch.uint8, sh[3], device)
+
+
+def act8_save(s: Shape, x, h, rt: Routing, store: ActStore8, dev_status=None, stream=None):
+    """usaf_act8_save: x [T,H] and h [2I,R_cap] of a forward into the store."""
+    d = x.device
+    _check_t("x", x, x.dtype, (s.T, s.H), d)
+    _check_t("h", h, x.dtype, ActStore8.shapes(s)[2], d)
+    store.check(s, d)
+    r = rt.c()
+    _check("usaf_act8_save", lib().usaf_act8_save(
+        ctypes.byref(s), _dt(x), _ptr(x), _ptr(h), ctypes.byref(r), _ptr(store.x_code),
+        _ptr(store.x_exp), _ptr(store.h_code), _ptr(store.h_exp), _ptr(dev_status),
+        _stream(stream)))
+
+
+def act8_restore(s: Shape, store: ActStore8, rt: Routing, x_perm, h, wa, x=None, stream=None):
+    """usaf_act8_restore: what the backward reads (x_perm, h, wa; x too unless None) from the
+    store and the routing of that forward."""
+    d, dt = h.device, h.dtype
+    cap = routed_rows_capacity(s)
+    store.check(s, d)
+    _check_t("x", x, dt, (s.T, s.H), d, optional=True)
+    _check_t("x_perm", x_perm, dt, (s.H, cap), d)
+    _check_t("h", h, dt, (2 * s.I, cap), d)
+    _check_t("wa", wa, dt, (s.I, cap), d)
+    r = rt.c()
+    _check("usaf_act8_restore", lib().usaf_act8_restore(
+        ctypes.byref(s), _dt(h), _ptr(store.x_code), _ptr(store.x_exp), _ptr(store.h_code),
+        _ptr(store.h_exp), ctypes.byref(r), _ptr(x), _ptr(x_perm), _ptr(h), _ptr(wa),
+        _stream(stream)))
 
 
 def trace_enable(on: bool) -> None:

@@ -1,0 +1,72 @@
+// Internal launch interfaces of the calls declared in usaf_train.h.
+#pragma once
+
+#include "common.cuh"
+#include "usaf_train.h"
+
+namespace usaf {
+
+// ---------------------------------------------------------------- router auxiliary losses
+struct AuxArgs {
+  int64_t T, G, ld;
+  int E, k;
+  const float* logits;
+  const int32_t* topk_idx;
+  const uint8_t* mask;    // [T] or null
+  const int32_t* offset;  // [G+1] or null (one group)
+  double coef_balance, coef_z;
+  uint32_t* status;
+};
+// Partial sums of the forward: a chunk of tokens and a group that meet own slot chunk + group
+// (each step along the tokens moves to the next chunk, the next group or both, so no two share one).
+struct AuxWs {
+  float* prob;  // [slots][E]
+  int32_t* count;
+  int32_t* n;  // [slots]
+  float* z;
+};
+int64_t aux_chunk_tokens(int64_t T);  // tokens of a chunk
+void aux_ws_layout(int64_t T, int64_t E, int64_t G, Carver& c, AuxWs& w);
+usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, int32_t* n_tok,
+                           float* loss, const AuxWs& w, cudaStream_t st);
+usaf_status aux_bwd_launch(const AuxArgs& a, const int32_t* count, const int32_t* n_tok,
+                           const float* d_loss, float* dlogit, int64_t ld_out, int accumulate,
+                           cudaStream_t st);
+
+// ---------------------------------------------------------------- router gradient products
+struct RouterGradArgs {
+  int64_t T, E, H, ld;
+  usaf_dtype dt;
+  const float* dlogit;
+  const void* x;
+  const float* w_router;
+  const float* g_in;
+  float* g_router;
+  const void* dx_in;
+  void* dx;
+  uint32_t* status;
+};
+struct RouterGradWs {
+  float* g_part;  // [splits][E][H] sums of g_router over parts of the tokens
+};
+void router_grad_ws_layout(int64_t T, int64_t E, int64_t H, usaf_dtype dt, Carver& c,
+                           RouterGradWs& w);
+usaf_status router_grad_launch(const RouterGradArgs& a, const RouterGradWs& w, cudaStream_t st);
+
+// ---------------------------------------------------------------- 8-bit activation store
+struct Act8Args {
+  usaf_moe_shape s;
+  usaf_dtype dt;
+  int64_t R_cap;
+  usaf_routing rt;
+  int8_t* x_code;
+  uint8_t* x_exp;
+  int8_t* h_code;
+  uint8_t* h_exp;
+};
+usaf_status act8_save_launch(const Act8Args& a, const void* x, const void* h, uint32_t* status,
+                             cudaStream_t st);
+usaf_status act8_restore_launch(const Act8Args& a, void* x_out, void* x_perm, void* h, void* wa,
+                                cudaStream_t st);
+
+}  // namespace usaf
