@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT, "libusaf.so")
 SOURCES = ["abi.cu", "route.cu", "moe.cu", "moe_tc.cu", "adam.cu", "select.cu", "noalloc.cu",
-           "abi_train.cu", "router_aux.cu", "router_grad.cu", "act8.cu"]
+           "abi_train.cu", "router_aux.cu", "router_grad.cu", "router_grad_tc.cu",
+           "act8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -138,41 +138,43 @@ int64_t splits_for(int64_t T, int64_t E, int64_t H) {
   return s < 1 ? 1 : s;
 }
 
-template <typename T>
-usaf_status launch_simt(const RouterGradArgs& a, const RouterGradWs& w, cudaStream_t st) {
-  if (a.g_router) {
-    const int64_t s = splits_for(a.T, a.E, a.H);
-    const int64_t per = round_up(ceil_div(a.T, s), RG_T);
-    const dim3 grid((unsigned)ceil_div(a.H, RG_H), (unsigned)ceil_div(a.E, RG_E),
-                    (unsigned)ceil_div(a.T, per));
-    {
-      USAF_TRACE("router_grad_w", st);
-      router_grad_w_kernel<T><<<grid, 256, 0, st>>>(a, per, w.g_part);
-      USAF_CHECK_LAUNCH();
-    }
-    if (grid.z > 1) {
-      USAF_TRACE("router_grad_reduce", st);
-      router_grad_reduce_kernel<<<grid_dim_for(a.E * a.H), 256, 0, st>>>(a, w.g_part,
-                                                                         (int)grid.z);
-      USAF_CHECK_LAUNCH();
-    }
+usaf_status launch_reduce(const RouterGradArgs& a, const float* part, int64_t splits,
+                          cudaStream_t st) {
+  USAF_TRACE("router_grad_reduce", st);
+  router_grad_reduce_kernel<<<grid_dim_for(a.E * a.H), 256, 0, st>>>(a, part, (int)splits);
+  USAF_CHECK_LAUNCH();
+  return USAF_OK;
+}
+
+usaf_status launch_w(const RouterGradArgs& a, float* part, cudaStream_t st) {
+  const int64_t s = splits_for(a.T, a.E, a.H);
+  const int64_t per = round_up(ceil_div(a.T, s), RG_T);
+  const dim3 grid((unsigned)ceil_div(a.H, RG_H), (unsigned)ceil_div(a.E, RG_E),
+                  (unsigned)ceil_div(a.T, per));
+  {
+    USAF_TRACE("router_grad_w", st);
+    router_grad_w_kernel<float><<<grid, 256, 0, st>>>(a, per, part);
+    USAF_CHECK_LAUNCH();
   }
-  if (a.dx) {
-    USAF_TRACE("router_grad_x", st);
-    const int64_t rows = ceil_div(a.T, DX_T);
-    // the grid's y axis holds 65,535 blocks: longer token axes go in several launches
-    for (int64_t r0 = 0; r0 < rows; r0 += 65535) {
-      RouterGradArgs b = a;
-      const int64_t skip = r0 * DX_T;
-      b.T = a.T - skip;
-      b.dlogit = a.dlogit + skip * a.ld;
-      b.dx_in = a.dx_in ? static_cast<const T*>(a.dx_in) + skip * a.H : nullptr;
-      b.dx = static_cast<T*>(a.dx) + skip * a.H;
-      const int64_t n = rows - r0 < 65535 ? rows - r0 : 65535;
-      if (b.T > n * DX_T) b.T = n * DX_T;
-      router_grad_x_kernel<T><<<dim3((unsigned)ceil_div(a.H, DX_H), (unsigned)n), 256, 0, st>>>(b);
-      USAF_CHECK_LAUNCH();
-    }
+  return grid.z > 1 ? launch_reduce(a, part, grid.z, st) : USAF_OK;
+}
+
+template <typename T>
+usaf_status launch_x(const RouterGradArgs& a, cudaStream_t st) {
+  USAF_TRACE("router_grad_x", st);
+  const int64_t rows = ceil_div(a.T, DX_T);
+  // the grid's y axis holds 65,535 blocks: longer token axes go in several launches
+  for (int64_t r0 = 0; r0 < rows; r0 += 65535) {
+    RouterGradArgs b = a;
+    const int64_t skip = r0 * DX_T;
+    b.T = a.T - skip;
+    b.dlogit = a.dlogit + skip * a.ld;
+    b.dx_in = a.dx_in ? static_cast<const T*>(a.dx_in) + skip * a.H : nullptr;
+    b.dx = static_cast<T*>(a.dx) + skip * a.H;
+    const int64_t n = rows - r0 < 65535 ? rows - r0 : 65535;
+    if (b.T > n * DX_T) b.T = n * DX_T;
+    router_grad_x_kernel<T><<<dim3((unsigned)ceil_div(a.H, DX_H), (unsigned)n), 256, 0, st>>>(b);
+    USAF_CHECK_LAUNCH();
   }
   return USAF_OK;
 }
@@ -181,12 +183,24 @@ usaf_status launch_simt(const RouterGradArgs& a, const RouterGradWs& w, cudaStre
 
 void router_grad_ws_layout(int64_t T, int64_t E, int64_t H, usaf_dtype dt, Carver& c,
                            RouterGradWs& w) {
-  const int64_t s = splits_for(T, E, H);
+  const int64_t s = dt == USAF_BF16 ? ceil_div(T, router_grad_tc_split(T, E, H))
+                                    : splits_for(T, E, H);
   w.g_part = c.take<float>(s > 1 ? s * E * H : 1);
 }
 
 usaf_status router_grad_launch(const RouterGradArgs& a, const RouterGradWs& w, cudaStream_t st) {
-  return a.dt == USAF_BF16 ? launch_simt<__nv_bfloat16>(a, w, st) : launch_simt<float>(a, w, st);
+  if (a.dt == USAF_F32) {
+    if (a.g_router) USAF_TRY(launch_w(a, w.g_part, st));
+    return a.dx ? launch_x<float>(a, st) : USAF_OK;
+  }
+  if (a.g_router) {
+    const int64_t per = router_grad_tc_split(a.T, a.E, a.H);
+    USAF_TRY(router_grad_w_tc(a, w.g_part, per, st));
+    if (per < a.T) USAF_TRY(launch_reduce(a, w.g_part, ceil_div(a.T, per), st));
+  }
+  if (!a.dx) return USAF_OK;
+  // the tensor-core kernel keeps the router's columns of at most 256 experts in shared memory
+  return router_grad_x_tc_ok(a.E) ? router_grad_x_tc(a, st) : launch_x<__nv_bfloat16>(a, st);
 }
 
 }  // namespace usaf
