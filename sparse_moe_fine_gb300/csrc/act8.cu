@@ -1,6 +1,13 @@
 // Activations in 8 bits between a layer's forward and its backward (usaf_act8_save / _restore):
 // blocks of 16 values share a power-of-two scale, so that coding and decoding are exact up to the
-// one rounding of each code, and every decoded value is a bf16 number.
+// one rounding of each code, and every decoded value is a bf16 number (a code has 7 bits).
+//
+// Both directions are bound by memory traffic: every value is read once and written once, whole
+// 16-byte vectors a lane, neighbouring lanes neighbouring vectors. The arithmetic stays at a few
+// instructions a value by two uses of fp32's exact integers: adding 1.5 * 2^23 leaves a rounded
+// (to nearest even) code in the low byte, and a code byte put into 2^23's mantissa is the code plus
+// a constant.
+#include "tc_ptx.cuh"
 #include "train.cuh"
 
 namespace usaf {
@@ -8,7 +15,8 @@ namespace usaf {
 namespace {
 
 constexpr int BLK = USAF_ACT8_BLOCK;
-constexpr int XG_ROWS = 128;  // permuted rows of a gather tile (x 64 features)
+constexpr int THREADS = 256;
+constexpr float MAX_CODED = 127.f * 2.6584559915698317e36f;  // 127 * 2^121
 
 // exponent byte of a block from its largest magnitude's fp32 bits: amax = m 2^q with 1 <= m < 2 is
 // covered by 127 * 2^(q - 6) while m <= 127 / 64; 0 for zeros, 255 for NaN and infinities
@@ -26,13 +34,102 @@ __device__ __forceinline__ float code_factor(int byte) {
 __device__ __forceinline__ float value_factor(int byte) {
   return __uint_as_float((uint32_t)byte << 23);
 }
-__device__ __forceinline__ int code_of(float v, float f) {
-  if (f == 0.f) return 0;
-  const int c = __float2int_rn(v * f);  // v * f is exact: f is a power of two
-  return c > 127 ? 127 : (c < -127 ? -127 : c);
+
+// ------------------------------------------------------------------------------ coding
+// v * f rounded to an integer, in the low byte (v * f is exact: f is a power of two)
+__device__ __forceinline__ uint32_t code_bits(float v, float f) {
+  return __float_as_uint(fmaf(v, f, 12582912.f));
+}
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+__device__ __forceinline__ float clamp_coded(float v) {
+  return fminf(fmaxf(v, -MAX_CODED), MAX_CODED);
 }
 
-// One block of n <= 16 consecutive values per thread.
+template <typename T>
+struct Vec;
+// 16 bytes: eight bf16 values, half a block (two lanes share it), eight codes
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  using Codes = uint2;
+  static __device__ __forceinline__ uint32_t amax(const uint4& r) {
+    const uint32_t k = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu),
+                                __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+    const uint32_t m = __vmaxu2(k, __shfl_xor_sync(0xffffffffu, k, 1));
+    return max(m >> 16, m & 0xFFFFu) << 16;
+  }
+  static __device__ __forceinline__ Codes encode(const uint4& r, int byte) {
+    const float f = code_factor(byte);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
+      if (byte == 248) lo = clamp_coded(lo), hi = clamp_coded(hi);
+      c[2 * i] = code_bits(lo, f);
+      c[2 * i + 1] = code_bits(hi, f);
+    }
+    if (byte == 255) return make_uint2(0, 0);
+    return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+  }
+};
+// four fp32 values, a quarter of a block, four codes
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  using Codes = uint32_t;
+  static __device__ __forceinline__ uint32_t amax(const uint4& r) {
+    uint32_t k = max(max(r.x & 0x7FFFFFFFu, r.y & 0x7FFFFFFFu),
+                     max(r.z & 0x7FFFFFFFu, r.w & 0x7FFFFFFFu));
+    k = max(k, __shfl_xor_sync(0xffffffffu, k, 1));
+    return max(k, __shfl_xor_sync(0xffffffffu, k, 2));
+  }
+  static __device__ __forceinline__ Codes encode(const uint4& r, int byte) {
+    const float f = code_factor(byte);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v = __uint_as_float(w[i]);
+      if (byte == 248) v = clamp_coded(v);
+      c[i] = code_bits(v, f);
+    }
+    return byte == 255 ? 0u : pack4(c[0], c[1], c[2], c[3]);
+  }
+};
+
+// n vectors (whole blocks) of src from vector i0 on, 32 lanes x U at a time: the warp's share of a
+// row. Every lane takes part; true where a block was not finite.
+template <typename T, int U>
+__device__ __forceinline__ bool encode_run(const T* src, int64_t i0, int64_t n, int8_t* code,
+                                           uint8_t* ex) {
+  using V = Vec<T>;
+  const int lane = threadIdx.x & 31;
+  uint4 r[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = i0 + u * 32 + lane;
+    r[u] = i < n ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+  }
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = i0 + u * 32 + lane;
+    const int b = exp_byte(V::amax(r[u]));
+    const typename V::Codes c = V::encode(r[u], b);
+    if (i < n) {
+      reinterpret_cast<typename V::Codes*>(code)[i] = c;
+      constexpr int LB = BLK / V::N;
+      if (i % LB == 0) ex[i / LB] = (uint8_t)b;
+      bad |= b == 255;
+    }
+  }
+  return bad;
+}
+
+// One block of n <= 16 values, a thread each: rows whose length is not a multiple of 16.
 template <typename T>
 __device__ __forceinline__ bool encode_block(const T* src, int n, int8_t* code, uint8_t* ex) {
   float v[BLK];
@@ -46,73 +143,249 @@ __device__ __forceinline__ bool encode_block(const T* src, int n, int8_t* code, 
   const float f = code_factor(b);
 #pragma unroll
   for (int i = 0; i < BLK; ++i)
-    if (i < n) code[i] = (int8_t)code_of(v[i], f);
+    if (i < n) code[i] = b == 255 ? (int8_t)0 : (int8_t)code_bits(clamp_coded(v[i]), f);
   *ex = (uint8_t)b;
   return b == 255;
 }
 
+constexpr int SAVE_U = 4;  // vectors of a lane in flight
+
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(THREADS)
     act8_save_kernel(const Act8Args a, const T* __restrict__ x, const T* __restrict__ h,
                      uint32_t* status) {
-  const int64_t stride = (int64_t)gridDim.x * 256, i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  constexpr int VW = Vec<T>::N, RUN = 32 * SAVE_U;  // vectors of a warp's run
+  const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
+  const int64_t wg = (int64_t)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;
   bool bad = false;
-  const int64_t nbx = (a.s.H + BLK - 1) / BLK;
-  for (int64_t i = i0; i < a.s.T * nbx; i += stride) {
-    const int64_t t = i / nbx, b = i - t * nbx;
-    const int64_t o = t * a.s.H + b * BLK;
-    bad |= encode_block(x + o, (int)min((int64_t)BLK, a.s.H - b * BLK), a.x_code + o, a.x_exp + i);
+  // h: each feature's rows that experts own, in runs
+  const int64_t nv = a.rt.expert_offset[a.s.E] / VW, pitch = a.R_cap / BLK;
+  const int64_t runs = (nv + RUN - 1) / RUN;
+  for (int64_t i = wg; i < 2 * a.s.I * runs; i += warps) {
+    const int64_t j = i / runs, r = i - j * runs;
+    bad |= encode_run<T, SAVE_U>(h + j * a.R_cap, r * RUN, nv, a.h_code + j * a.R_cap,
+                                 a.h_exp + j * pitch);
   }
-  const int64_t nb = a.rt.expert_offset[a.s.E] / BLK, pitch = a.R_cap / BLK;
-  for (int64_t i = i0; i < 2 * a.s.I * nb; i += stride) {
-    const int64_t j = i / nb, b = i - j * nb;
-    const int64_t o = j * a.R_cap + b * BLK;
-    bad |= encode_block(h + o, BLK, a.h_code + o, a.h_exp + j * pitch + b);
+  // x: tokens of whole blocks are one run of vectors
+  if (a.s.H % BLK == 0) {
+    const int64_t n = a.s.T * a.s.H / VW;
+    for (int64_t i = wg * RUN; i < n; i += warps * RUN)
+      bad |= encode_run<T, SAVE_U>(x, i, n, a.x_code, a.x_exp);
+  } else {
+    const int64_t nbx = (a.s.H + BLK - 1) / BLK;
+    for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < a.s.T * nbx;
+         i += (int64_t)gridDim.x * THREADS) {
+      const int64_t t = i / nbx, b = i - t * nbx;
+      const int64_t o = t * a.s.H + b * BLK;
+      bad |= encode_block(x + o, (int)min((int64_t)BLK, a.s.H - b * BLK), a.x_code + o,
+                          a.x_exp + i);
+    }
   }
   flag_status_warp(status, bad, USAF_DEV_NONFINITE);
 }
 
-// silu by exp(-|g|), which does not overflow: far negative gates keep their tiny values
-__device__ __forceinline__ float silu_tail(float g) {
-  const float e = expf(-fabsf(g));
-  return g * (g >= 0.f ? 1.f : e) / (1.f + e);
+// ------------------------------------------------------------------------------ decoding
+// the four codes of a word as floats: byte q ^ 0x80 in the mantissa of 2^23 is 2^23 + 128 + code
+__device__ __forceinline__ void decode4(uint32_t w, float s, float* v) {
+  const uint32_t u = w ^ 0x80808080u;
+  v[0] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)) - 8388736.f) * s;
+  v[1] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - 8388736.f) * s;
+  v[2] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - 8388736.f) * s;
+  v[3] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - 8388736.f) * s;
+}
+template <typename T>
+__device__ __forceinline__ void decode(const typename Vec<T>::Codes& c, float s,
+                                       float (&v)[Vec<T>::N]) {
+  if constexpr (Vec<T>::N == 8) {
+    decode4(c.x, s, v);
+    decode4(c.y, s, v + 4);
+  } else {
+    decode4(c, s, v);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 to_vec(const float (&v)[Vec<T>::N]) {
+  if constexpr (Vec<T>::N == 8) {
+    return make_uint4(tcx::pack_bf16x2(v[0], v[1]), tcx::pack_bf16x2(v[2], v[3]),
+                      tcx::pack_bf16x2(v[4], v[5]), tcx::pack_bf16x2(v[6], v[7]));
+  } else {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  }
 }
 
+// silu by exp(-|g|), which does not overflow: far negative gates keep their tiny values. bf16
+// results are rounded to 8 bits, so the fast exponential and quotient (2^-20 and better on the
+// gates that a rounded result can tell apart) serve them.
 template <typename T>
-__global__ void __launch_bounds__(256)
-    act8_restore_rows_kernel(const Act8Args a, T* __restrict__ x_out, T* __restrict__ h,
-                             T* __restrict__ wa) {
-  const int64_t stride = (int64_t)gridDim.x * 256, i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (x_out) {
-    const int64_t nbx = (a.s.H + BLK - 1) / BLK;
-    for (int64_t i = i0; i < a.s.T * a.s.H; i += stride) {
-      const int64_t t = i / a.s.H, c = i - t * a.s.H;
-      x_out[i] = from_f32<T>((float)a.x_code[i] * value_factor(a.x_exp[t * nbx + c / BLK]));
+__device__ __forceinline__ float silu_tail(float g) {
+  if constexpr (sizeof(T) == 2) {
+    const float e = __expf(-fabsf(g));
+    return g * (g >= 0.f ? 1.f : e) * __fdividef(1.f, 1.f + e);
+  } else {
+    const float e = expf(-fabsf(g));
+    return g * (g >= 0.f ? 1.f : e) / (1.f + e);
+  }
+}
+
+// Rows [seg, seg + 32 vectors) of `nf` features from feature `f0` on, one warp a feature: h decoded,
+// wa formed again. The lanes' routing weights stay in registers over the features.
+constexpr int ROW_FEATURES = 64;  // features of a block: eight per warp
+template <typename T>
+__device__ __forceinline__ void restore_rows(const Act8Args& a, int64_t seg, int64_t f0, T* h,
+                                             T* wa) {
+  using V = Vec<T>;
+  constexpr int VW = V::N;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int64_t rows = a.rt.expert_offset[a.s.E], r = seg + lane * VW;
+  if (seg >= rows) return;
+  const bool in = r < rows;  // rows is a multiple of 16: a vector is whole or not there
+  float w[VW];
+#pragma unroll
+  for (int q = 0; q < VW; q += 4) {
+    const int4 sl = in ? *reinterpret_cast<const int4*>(a.rt.perm_slot + r + q)
+                       : make_int4(-1, -1, -1, -1);
+    w[q] = sl.x >= 0 ? a.rt.topk_w[sl.x] : 0.f;
+    w[q + 1] = sl.y >= 0 ? a.rt.topk_w[sl.y] : 0.f;
+    w[q + 2] = sl.z >= 0 ? a.rt.topk_w[sl.z] : 0.f;
+    w[q + 3] = sl.w >= 0 ? a.rt.topk_w[sl.w] : 0.f;
+  }
+  if (!in) return;
+  const int64_t pitch = a.R_cap / BLK;
+  constexpr int U = 2;  // features of a warp in flight
+#pragma unroll 1
+  for (int f = wid; f < ROW_FEATURES; f += 8 * U) {
+    typename V::Codes cg[U], cu[U];
+    float sg[U], su[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = f0 + f + 8 * u;
+      if (i < a.s.I) {
+        const int64_t og = i * a.R_cap + r, ou = (a.s.I + i) * a.R_cap + r;
+        cg[u] = __ldg(reinterpret_cast<const typename V::Codes*>(a.h_code + og));
+        cu[u] = __ldg(reinterpret_cast<const typename V::Codes*>(a.h_code + ou));
+        sg[u] = value_factor(__ldg(a.h_exp + i * pitch + r / BLK));
+        su[u] = value_factor(__ldg(a.h_exp + (a.s.I + i) * pitch + r / BLK));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = f0 + f + 8 * u;
+      if (i >= a.s.I) break;
+      const int64_t og = i * a.R_cap + r, ou = (a.s.I + i) * a.R_cap + r;
+      float g[VW], up[VW];
+      decode<T>(cg[u], sg[u], g);
+      decode<T>(cu[u], su[u], up);
+      *reinterpret_cast<uint4*>(h + og) = to_vec<T>(g);
+      *reinterpret_cast<uint4*>(h + ou) = to_vec<T>(up);
+#pragma unroll
+      for (int q = 0; q < VW; ++q) g[q] = w[q] * silu_tail<T>(g[q]) * up[q];
+      *reinterpret_cast<uint4*>(wa + og) = to_vec<T>(g);
     }
   }
-  const int64_t rows = a.rt.expert_offset[a.s.E], pitch = a.R_cap / BLK;
-  for (int64_t i = i0; i < a.s.I * rows; i += stride) {
-    const int64_t j = i / rows, r = i - j * rows;
-    const int64_t og = j * a.R_cap + r, ou = (a.s.I + j) * a.R_cap + r;
-    const float g = (float)a.h_code[og] * value_factor(a.h_exp[j * pitch + r / BLK]);
-    const float u = (float)a.h_code[ou] * value_factor(a.h_exp[(a.s.I + j) * pitch + r / BLK]);
-    const int slot = a.rt.perm_slot[r];
-    const float w = slot >= 0 ? a.rt.topk_w[slot] : 0.f;
-    h[og] = from_f32<T>(g);
-    h[ou] = from_f32<T>(u);
-    wa[og] = from_f32<T>(w * silu_tail(g) * u);
+}
+
+constexpr int X_VECTORS = 4 * THREADS;  // vectors of a block of the decoded x
+template <typename T>
+__device__ __forceinline__ void restore_x(const Act8Args& a, int64_t blk, T* x) {
+  using V = Vec<T>;
+  if (a.s.H % BLK == 0) {
+    const int64_t n = a.s.T * a.s.H / V::N;
+    typename V::Codes c[4];
+    float s[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = blk * X_VECTORS + u * THREADS + threadIdx.x;
+      if (i < n) {
+        c[u] = __ldg(reinterpret_cast<const typename V::Codes*>(a.x_code) + i);
+        s[u] = value_factor(__ldg(a.x_exp + i / (BLK / V::N)));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = blk * X_VECTORS + u * THREADS + threadIdx.x;
+      if (i >= n) break;
+      float v[V::N];
+      decode<T>(c[u], s[u], v);
+      reinterpret_cast<uint4*>(x)[i] = to_vec<T>(v);
+    }
+  } else {
+    const int64_t nbx = (a.s.H + BLK - 1) / BLK, lo = blk * X_VECTORS * V::N;
+    const int64_t hi = min(a.s.T * a.s.H, lo + X_VECTORS * V::N);
+    for (int64_t i = lo + threadIdx.x; i < hi; i += THREADS) {
+      const int64_t t = i / a.s.H, c = i - t * a.s.H;
+      x[i] = from_f32<T>((float)a.x_code[i] * value_factor(a.x_exp[t * nbx + c / BLK]));
+    }
   }
 }
 
-// x_perm[f, row] = the decoded x of the row's token, 0 in padding and tail rows
+// x_perm[f, row] = the decoded x of the row's token, 0 in padding and tail rows: 256 rows x 64
+// features, stored by TMA as four boxes of 64 rows x 64 features. A lane decodes eight rows x eight
+// features and packs the transpose as it converts (a bf16 pair is one feature of two rows). The
+// eight lanes of a quarter-warp write eight row chunks of one feature, so every 16-byte store into
+// the 128-byte swizzled box is free of bank conflicts, and a row's four feature groups are one
+// 32-byte sector of codes. H a multiple of 64.
+constexpr int G_ROWS = 256, G_FEATURES = 64;
+constexpr int G_SMEM = 4 * 8192 + 1024;
+__device__ __forceinline__ void gather_bf16(const CUtensorMap& tm, const Act8Args& a, int64_t rb,
+                                            int fb, uint8_t* tile) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int c = lane & 7, box = wid >> 1;
+  const int f = (wid & 1) * 32 + (lane >> 3) * 8;  // first feature within the block's 64
+  const int64_t r = rb * G_ROWS + box * 64 + c * 8;
+  const int64_t rows = a.rt.expert_offset[a.s.E], nbx = a.s.H / BLK;
+  const int f0 = fb * G_FEATURES + f;
+  uint2 code[8];
+  float s[8];
+  {
+    const int4 t0 = *reinterpret_cast<const int4*>(a.rt.perm_tok + r);
+    const int4 t1 = *reinterpret_cast<const int4*>(a.rt.perm_tok + r + 4);
+    const int4 s0 = *reinterpret_cast<const int4*>(a.rt.perm_slot + r);
+    const int4 s1 = *reinterpret_cast<const int4*>(a.rt.perm_slot + r + 4);
+    const int tok[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+    const int slot[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool live = r < rows && slot[i] >= 0;
+      code[i] = live ? __ldg(reinterpret_cast<const uint2*>(a.x_code + tok[i] * a.s.H + f0))
+                     : make_uint2(0, 0);
+      s[i] = live ? value_factor(__ldg(a.x_exp + tok[i] * nbx + f0 / BLK)) : 0.f;
+    }
+  }
+  uint32_t out[8][4];  // [feature][pair of rows]
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    float v0[8], v1[8];
+    decode<__nv_bfloat16>(code[2 * p], s[2 * p], v0);
+    decode<__nv_bfloat16>(code[2 * p + 1], s[2 * p + 1], v1);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) out[k][p] = tcx::pack_bf16x2(v0[k], v1[k]);
+  }
+  uint8_t* bx = tile + box * 8192 + f * 128;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<uint4*>(bx + k * 128 + ((c ^ k) << 4)) =
+        make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+  tcx::fence_async_smem();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t src = tcx::smem_u32(tile);
+    for (int b = 0; b < 4; ++b)
+      tcx::tma_store_2d(&tm, src + b * 8192, (int)(rb * G_ROWS + b * 64), fb * G_FEATURES);
+    tcx::bulk_commit();
+    tcx::bulk_wait();
+  }
+}
+
+// The same for fp32 tokens and for widths that are no multiple of 64.
+constexpr int XG_ROWS = 128;
 template <typename T>
-__global__ void __launch_bounds__(256)
-    act8_gather_kernel(const Act8Args a, T* __restrict__ x_perm) {
+__global__ void __launch_bounds__(THREADS) act8_gather_kernel(const Act8Args a, T* x_perm) {
   __shared__ T tile[64][XG_ROWS + 1];
   const int64_t r0 = (int64_t)blockIdx.x * XG_ROWS;
   const int64_t h0 = (int64_t)blockIdx.y * 64;
   const int64_t end = a.rt.expert_offset[a.s.E], nbx = (a.s.H + BLK - 1) / BLK;
-  for (int v = threadIdx.x; v < XG_ROWS * 64; v += 256) {
+  for (int v = threadIdx.x; v < XG_ROWS * 64; v += THREADS) {
     const int r = v / 64, f = v % 64;
     const int64_t row = r0 + r, c = h0 + f;
     float val = 0.f;
@@ -123,24 +396,78 @@ __global__ void __launch_bounds__(256)
     tile[f][r] = from_f32<T>(val);
   }
   __syncthreads();
-  for (int v = threadIdx.x; v < XG_ROWS * 64; v += 256) {
+  for (int v = threadIdx.x; v < XG_ROWS * 64; v += THREADS) {
     const int f = v / XG_ROWS, r = v % XG_ROWS;
     if (h0 + f < a.s.H) x_perm[(h0 + f) * a.R_cap + r0 + r] = tile[f][r];
   }
 }
 
+// The blocks of one launch: gather tiles (GATHER), then rows of h and wa, then x.
+struct RestoreGrid {
+  int64_t gather_rows, gather, row_segs, rows, x;
+};
+
+#ifndef MINB
+#define MINB 3
+#endif
+template <typename T, bool GATHER>
+__global__ void __launch_bounds__(THREADS, MINB)
+    act8_restore_kernel(const __grid_constant__ CUtensorMap tm, const Act8Args a,
+                        const RestoreGrid g, T* x_out, T* h, T* wa) {
+  extern __shared__ uint8_t raw[];
+  int64_t b = blockIdx.x;
+  if constexpr (GATHER) {
+    if (b < g.gather) {
+      uint8_t* tile = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                                 ~uintptr_t(1023));
+      const int64_t fb = b / g.gather_rows;
+      gather_bf16(tm, a, b - fb * g.gather_rows, (int)fb, tile);
+      return;
+    }
+    b -= g.gather;
+  }
+  if (b < g.rows) {
+    const int64_t fb = b / g.row_segs;
+    restore_rows<T>(a, (b - fb * g.row_segs) * 32 * Vec<T>::N, fb * ROW_FEATURES, h, wa);
+    return;
+  }
+  restore_x<T>(a, b - g.rows, x_out);
+}
+
 template <typename T>
 usaf_status restore(const Act8Args& a, void* x_out, void* x_perm, void* h, void* wa,
                     cudaStream_t st) {
+  CUtensorMap tm{};
+  RestoreGrid g{};
+  const bool tiles = sizeof(T) == 2 && a.s.H % G_FEATURES == 0;
+  if (tiles) {
+    if (!tcx::map_bf16_2d(&tm, x_perm, a.R_cap, a.s.H, 64, 64)) return USAF_ERR_CUDA;
+    g.gather_rows = a.R_cap / G_ROWS;
+    g.gather = g.gather_rows * (a.s.H / G_FEATURES);
+  }
+  g.row_segs = ceil_div(a.R_cap, 32 * Vec<T>::N);
+  g.rows = g.row_segs * ceil_div(a.s.I, ROW_FEATURES);
+  g.x = x_out ? ceil_div(a.s.T * a.s.H, X_VECTORS * Vec<T>::N) : 0;
+  const int64_t blocks = g.gather + g.rows + g.x;
+  if (blocks >= (int64_t(1) << 31)) return USAF_ERR_UNSUPPORTED;
   {
-    USAF_TRACE("act8_restore_rows", st);
-    act8_restore_rows_kernel<T><<<grid_dim_for(a.s.I * a.R_cap), 256, 0, st>>>(
-        a, static_cast<T*>(x_out), static_cast<T*>(h), static_cast<T*>(wa));
+    USAF_TRACE("act8_restore", st);
+    T *xo = static_cast<T*>(x_out), *ho = static_cast<T*>(h), *wo = static_cast<T*>(wa);
+    if constexpr (sizeof(T) == 2) {
+      if (tiles)
+        act8_restore_kernel<T, true><<<(unsigned)blocks, THREADS, G_SMEM, st>>>(tm, a, g, xo, ho,
+                                                                                wo);
+      else
+        act8_restore_kernel<T, false><<<(unsigned)blocks, THREADS, 0, st>>>(tm, a, g, xo, ho, wo);
+    } else {
+      act8_restore_kernel<T, false><<<(unsigned)blocks, THREADS, 0, st>>>(tm, a, g, xo, ho, wo);
+    }
     USAF_CHECK_LAUNCH();
   }
+  if (tiles) return USAF_OK;
   USAF_TRACE("act8_gather", st);
   const dim3 grid((unsigned)(a.R_cap / XG_ROWS), (unsigned)ceil_div(a.s.H, 64));
-  act8_gather_kernel<T><<<grid, 256, 0, st>>>(a, static_cast<T*>(x_perm));
+  act8_gather_kernel<T><<<grid, THREADS, 0, st>>>(a, static_cast<T*>(x_perm));
   USAF_CHECK_LAUNCH();
   return USAF_OK;
 }
@@ -150,13 +477,17 @@ usaf_status restore(const Act8Args& a, void* x_out, void* x_perm, void* h, void*
 usaf_status act8_save_launch(const Act8Args& a, const void* x, const void* h, uint32_t* status,
                              cudaStream_t st) {
   USAF_TRACE("act8_save", st);
-  const unsigned grid = grid_dim_for((2 * a.s.I * a.R_cap + a.s.T * a.s.H) / BLK);
+  const int64_t vw = a.dt == USAF_BF16 ? 8 : 4;
+  const int64_t runs = 2 * a.s.I * ceil_div(a.R_cap / vw, 32 * SAVE_U) + ceil_div(a.s.T * a.s.H, 32 * SAVE_U * vw);
+  const int64_t most = 8 * 152;  // eight blocks of 256 threads fill an SM
+  const int64_t want = ceil_div(runs, THREADS / 32);
+  const unsigned grid = (unsigned)(want < most ? want : most);
   if (a.dt == USAF_BF16)
-    act8_save_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(
+    act8_save_kernel<__nv_bfloat16><<<grid, THREADS, 0, st>>>(
         a, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(h), status);
   else
-    act8_save_kernel<float><<<grid, 256, 0, st>>>(a, static_cast<const float*>(x),
-                                                  static_cast<const float*>(h), status);
+    act8_save_kernel<float><<<grid, THREADS, 0, st>>>(a, static_cast<const float*>(x),
+                                                      static_cast<const float*>(h), status);
   USAF_CHECK_LAUNCH();
   return USAF_OK;
 }
