@@ -60,6 +60,7 @@ struct Vec<__nv_bfloat16> {
     const uint32_t m = __vmaxu2(k, __shfl_xor_sync(0xffffffffu, k, 1));
     return max(m >> 16, m & 0xFFFFu) << 16;
   }
+  template <bool RARE>
   static __device__ __forceinline__ Codes encode(const uint4& r, int byte) {
     const float f = code_factor(byte);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -67,11 +68,11 @@ struct Vec<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
-      if (byte == 248) lo = clamp_coded(lo), hi = clamp_coded(hi);
+      if (RARE) lo = clamp_coded(lo), hi = clamp_coded(hi);
       c[2 * i] = code_bits(lo, f);
       c[2 * i + 1] = code_bits(hi, f);
     }
-    if (byte == 255) return make_uint2(0, 0);
+    if (RARE && byte == 255) return make_uint2(0, 0);
     return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
   }
 };
@@ -86,6 +87,7 @@ struct Vec<float> {
     k = max(k, __shfl_xor_sync(0xffffffffu, k, 1));
     return max(k, __shfl_xor_sync(0xffffffffu, k, 2));
   }
+  template <bool RARE>
   static __device__ __forceinline__ Codes encode(const uint4& r, int byte) {
     const float f = code_factor(byte);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -93,40 +95,51 @@ struct Vec<float> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float v = __uint_as_float(w[i]);
-      if (byte == 248) v = clamp_coded(v);
+      if (RARE) v = clamp_coded(v);
       c[i] = code_bits(v, f);
     }
-    return byte == 255 ? 0u : pack4(c[0], c[1], c[2], c[3]);
+    return RARE && byte == 255 ? 0u : pack4(c[0], c[1], c[2], c[3]);
   }
 };
 
-// n vectors (whole blocks) of src from vector i0 on, 32 lanes x U at a time: the warp's share of a
-// row. Every lane takes part; true where a block was not finite.
+// The warp's 32 x U vectors of src from vector i0 on, of which those below n are there (n whole
+// blocks); every lane takes part. True where a block was not finite. Blocks at the top of fp32's
+// range, whose codes have to be clamped, and blocks that are not finite are coded on a path of
+// their own: their tests would cost the others a third more instructions.
 template <typename T, int U>
 __device__ __forceinline__ bool encode_run(const T* src, int64_t i0, int64_t n, int8_t* code,
                                            uint8_t* ex) {
   using V = Vec<T>;
+  using Codes = typename V::Codes;
+  constexpr int LB = BLK / V::N;
   const int lane = threadIdx.x & 31;
+  const int left = (int)min((int64_t)(32 * U), n - i0) - lane;  // vector 32 u + lane is there
+  const uint4* from = reinterpret_cast<const uint4*>(src) + i0 + lane;
+  Codes* to = reinterpret_cast<Codes*>(code) + i0 + lane;
+  uint8_t* eto = ex + (i0 + lane) / LB;
   uint4 r[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t i = i0 + u * 32 + lane;
-    r[u] = i < n ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
-  }
-  bool bad = false;
+  for (int u = 0; u < U; ++u)
+    r[u] = 32 * u < left ? __ldg(from + 32 * u) : make_uint4(0, 0, 0, 0);
+  int b[U];
+  int top = 0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t i = i0 + u * 32 + lane;
-    const int b = exp_byte(V::amax(r[u]));
-    const typename V::Codes c = V::encode(r[u], b);
-    if (i < n) {
-      reinterpret_cast<typename V::Codes*>(code)[i] = c;
-      constexpr int LB = BLK / V::N;
-      if (i % LB == 0) ex[i / LB] = (uint8_t)b;
-      bad |= b == 255;
+    b[u] = exp_byte(V::amax(r[u]));
+    top = max(top, b[u]);
+  }
+  const bool rare = __any_sync(0xffffffffu, top >= 248);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    Codes c;
+    if (!rare) c = V::template encode<false>(r[u], b[u]);
+    else c = V::template encode<true>(r[u], b[u]);
+    if (32 * u < left) {
+      to[32 * u] = c;
+      if (lane % LB == 0) eto[32 / LB * u] = (uint8_t)b[u];
     }
   }
-  return bad;
+  return top == 255;
 }
 
 // One block of n <= 16 values, a thread each: rows whose length is not a multiple of 16.
@@ -251,37 +264,47 @@ __device__ __forceinline__ void restore_rows(const Act8Args& a, int64_t seg, int
     w[q + 3] = sl.w >= 0 ? a.rt.topk_w[sl.w] : 0.f;
   }
   if (!in) return;
-  const int64_t pitch = a.R_cap / BLK;
-  constexpr int U = 2;  // features of a warp in flight
+  using Codes = typename V::Codes;
+  constexpr int U = 2;  // features of a warp in flight (1 and 4: 9% and 13% slower)
+  // the lane's places in the gate's row of this warp's first feature
+  const int fw = __shfl_sync(__activemask(), wid, 0);
+  const int64_t i0 = f0 + fw, pitch = a.R_cap / BLK;
+  const int8_t* gc = a.h_code + i0 * a.R_cap + r;
+  const uint8_t* ge = a.h_exp + i0 * pitch + r / BLK;
+  T* gh = h + i0 * a.R_cap + r;
+  T* gw = wa + i0 * a.R_cap + r;
+  const int64_t up_c = a.s.I * a.R_cap, up_e = a.s.I * pitch;
+  const int nf = (int)min((int64_t)ROW_FEATURES, a.s.I - f0);
 #pragma unroll 1
-  for (int f = wid; f < ROW_FEATURES; f += 8 * U) {
-    typename V::Codes cg[U], cu[U];
-    float sg[U], su[U];
+  for (int f = fw; f < nf; f += 8 * U) {
+    Codes cg[U], cu[U];
+    int sg[U], su[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = f0 + f + 8 * u;
-      if (i < a.s.I) {
-        const int64_t og = i * a.R_cap + r, ou = (a.s.I + i) * a.R_cap + r;
-        cg[u] = __ldg(reinterpret_cast<const typename V::Codes*>(a.h_code + og));
-        cu[u] = __ldg(reinterpret_cast<const typename V::Codes*>(a.h_code + ou));
-        sg[u] = value_factor(__ldg(a.h_exp + i * pitch + r / BLK));
-        su[u] = value_factor(__ldg(a.h_exp + (a.s.I + i) * pitch + r / BLK));
-      }
+      if (f + 8 * u >= nf) break;
+      cg[u] = __ldg(reinterpret_cast<const Codes*>(gc + 8 * u * a.R_cap));
+      cu[u] = __ldg(reinterpret_cast<const Codes*>(gc + 8 * u * a.R_cap + up_c));
+      sg[u] = __ldg(ge + 8 * u * pitch);
+      su[u] = __ldg(ge + 8 * u * pitch + up_e);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = f0 + f + 8 * u;
-      if (i >= a.s.I) break;
-      const int64_t og = i * a.R_cap + r, ou = (a.s.I + i) * a.R_cap + r;
+      if (f + 8 * u >= nf) break;
       float g[VW], up[VW];
-      decode<T>(cg[u], sg[u], g);
-      decode<T>(cu[u], su[u], up);
-      *reinterpret_cast<uint4*>(h + og) = to_vec<T>(g);
-      *reinterpret_cast<uint4*>(h + ou) = to_vec<T>(up);
+      decode<T>(cg[u], value_factor(sg[u]), g);
+      *reinterpret_cast<uint4*>(gh + 8 * u * a.R_cap) = to_vec<T>(g);
 #pragma unroll
-      for (int q = 0; q < VW; ++q) g[q] = w[q] * silu_tail<T>(g[q]) * up[q];
-      *reinterpret_cast<uint4*>(wa + og) = to_vec<T>(g);
+      for (int q = 0; q < VW; ++q) g[q] = w[q] * silu_tail<T>(g[q]);
+      decode<T>(cu[u], value_factor(su[u]), up);
+      *reinterpret_cast<uint4*>(gh + 8 * u * a.R_cap + up_c) = to_vec<T>(up);
+#pragma unroll
+      for (int q = 0; q < VW; ++q) g[q] *= up[q];
+      *reinterpret_cast<uint4*>(gw + 8 * u * a.R_cap) = to_vec<T>(g);
     }
+    gc += 8 * U * a.R_cap;
+    ge += 8 * U * pitch;
+    gh += 8 * U * a.R_cap;
+    gw += 8 * U * a.R_cap;
   }
 }
 
@@ -320,61 +343,82 @@ __device__ __forceinline__ void restore_x(const Act8Args& a, int64_t blk, T* x) 
 }
 
 // x_perm[f, row] = the decoded x of the row's token, 0 in padding and tail rows: 256 rows x 64
-// features, stored by TMA as four boxes of 64 rows x 64 features. A lane decodes eight rows x eight
-// features and packs the transpose as it converts (a bf16 pair is one feature of two rows). The
-// eight lanes of a quarter-warp write eight row chunks of one feature, so every 16-byte store into
-// the 128-byte swizzled box is free of bank conflicts, and a row's four feature groups are one
-// 32-byte sector of codes. H a multiple of 64.
-constexpr int G_ROWS = 256, G_FEATURES = 64;
+// features at a time, stored by TMA as four boxes of 64 rows x 64 features. A lane decodes eight rows
+// x eight features and packs the transpose as it converts (a bf16 pair is one feature of two rows).
+// The eight lanes of a quarter-warp write eight row chunks of one feature, so every 16-byte store
+// into the 128-byte swizzled box is free of bank conflicts, and a row's four feature groups are one
+// 32-byte sector of codes. A block keeps its rows' tokens over G_STEPS feature tiles; the copy engine
+// reads a tile while the next one's codes are on their way. H a multiple of 64.
+constexpr int G_ROWS = 256, G_FEATURES = 64, G_STEPS = 4;
 constexpr int G_SMEM = 4 * 8192 + 1024;
-__device__ __forceinline__ void gather_bf16(const CUtensorMap& tm, const Act8Args& a, int64_t rb,
-                                            int fb, uint8_t* tile) {
+__device__ __forceinline__ void gather_bf16(const CUtensorMap& tm, const Act8Args& a, int rb,
+                                            int fb0, uint8_t* tile) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int c = lane & 7, box = wid >> 1;
-  const int f = (wid & 1) * 32 + (lane >> 3) * 8;  // first feature within the block's 64
-  const int64_t r = rb * G_ROWS + box * 64 + c * 8;
-  const int64_t rows = a.rt.expert_offset[a.s.E], nbx = a.s.H / BLK;
-  const int f0 = fb * G_FEATURES + f;
-  uint2 code[8];
-  float s[8];
+  const int f = (wid & 1) * 32 + (lane >> 3) * 8;  // first feature within the tile's 64
+  const int64_t r = (int64_t)rb * G_ROWS + box * 64 + c * 8;
+  const int rows = a.rt.expert_offset[a.s.E], H = (int)a.s.H;
+  uint32_t at[8];  // the token's first vector of eight codes, NONE without one
+  constexpr uint32_t NONE = 0xFFFFFFFFu;
   {
     const int4 t0 = *reinterpret_cast<const int4*>(a.rt.perm_tok + r);
     const int4 t1 = *reinterpret_cast<const int4*>(a.rt.perm_tok + r + 4);
     const int4 s0 = *reinterpret_cast<const int4*>(a.rt.perm_slot + r);
     const int4 s1 = *reinterpret_cast<const int4*>(a.rt.perm_slot + r + 4);
-    const int tok[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
-    const int slot[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    const int tt[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+    const int ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool live = r < rows && slot[i] >= 0;
-      code[i] = live ? __ldg(reinterpret_cast<const uint2*>(a.x_code + tok[i] * a.s.H + f0))
-                     : make_uint2(0, 0);
-      s[i] = live ? value_factor(__ldg(a.x_exp + tok[i] * nbx + f0 / BLK)) : 0.f;
-    }
-  }
-  uint32_t out[8][4];  // [feature][pair of rows]
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    float v0[8], v1[8];
-    decode<__nv_bfloat16>(code[2 * p], s[2 * p], v0);
-    decode<__nv_bfloat16>(code[2 * p + 1], s[2 * p + 1], v1);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) out[k][p] = tcx::pack_bf16x2(v0[k], v1[k]);
+    for (int i = 0; i < 8; ++i)
+      at[i] = r < rows && ss[i] >= 0 ? (uint32_t)tt[i] * (uint32_t)(H / 8) : NONE;
   }
   uint8_t* bx = tile + box * 8192 + f * 128;
+  const int steps = min(G_STEPS, H / G_FEATURES - fb0);
+  const uint2* xc = reinterpret_cast<const uint2*>(a.x_code) + (fb0 * G_FEATURES + f) / 8;
+  const uint8_t* xe = a.x_exp + (fb0 * G_FEATURES + f) / BLK;
+#pragma unroll 1
+  for (int st = 0; st < steps; ++st) {
+    uint2 code[8];
+    int s[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    *reinterpret_cast<uint4*>(bx + k * 128 + ((c ^ k) << 4)) =
-        make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
-  tcx::fence_async_smem();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const uint32_t src = tcx::smem_u32(tile);
-    for (int b = 0; b < 4; ++b)
-      tcx::tma_store_2d(&tm, src + b * 8192, (int)(rb * G_ROWS + b * 64), fb * G_FEATURES);
-    tcx::bulk_commit();
-    tcx::bulk_wait();
+    for (int i = 0; i < 8; ++i) {
+      const bool live = at[i] != NONE;
+      code[i] = live ? __ldg(xc + at[i]) : make_uint2(0, 0);
+      s[i] = live ? __ldg(xe + (at[i] >> 1)) : 0;  // an exponent per two vectors
+    }
+    xc += G_FEATURES / 8;
+    xe += G_FEATURES / BLK;
+    if (st > 0) {  // the last tile has been read out of shared memory
+      if (threadIdx.x == 0) tcx::bulk_wait_read();
+      __syncthreads();
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {  // four features of the eight rows
+      uint32_t out[4][4];                   // [feature][pair of rows]
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        float v0[4], v1[4];
+        decode4(half ? code[2 * p].y : code[2 * p].x, value_factor(s[2 * p]), v0);
+        decode4(half ? code[2 * p + 1].y : code[2 * p + 1].x, value_factor(s[2 * p + 1]), v1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[k][p] = tcx::pack_bf16x2(v0[k], v1[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int fk = half * 4 + k;
+        *reinterpret_cast<uint4*>(bx + fk * 128 + ((c ^ fk) << 4)) =
+            make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+      }
+    }
+    tcx::fence_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const uint32_t src = tcx::smem_u32(tile);
+      for (int b = 0; b < 4; ++b)
+        tcx::tma_store_2d(&tm, src + b * 8192, rb * G_ROWS + b * 64, (fb0 + st) * G_FEATURES);
+      tcx::bulk_commit();
+    }
   }
+  if (threadIdx.x == 0) tcx::bulk_wait();
 }
 
 // The same for fp32 tokens and for widths that are no multiple of 64.
@@ -407,11 +451,8 @@ struct RestoreGrid {
   int64_t gather_rows, gather, row_segs, rows, x;
 };
 
-#ifndef MINB
-#define MINB 3
-#endif
 template <typename T, bool GATHER>
-__global__ void __launch_bounds__(THREADS, MINB)
+__global__ void __launch_bounds__(THREADS, 4)
     act8_restore_kernel(const __grid_constant__ CUtensorMap tm, const Act8Args a,
                         const RestoreGrid g, T* x_out, T* h, T* wa) {
   extern __shared__ uint8_t raw[];
@@ -420,8 +461,8 @@ __global__ void __launch_bounds__(THREADS, MINB)
     if (b < g.gather) {
       uint8_t* tile = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                                  ~uintptr_t(1023));
-      const int64_t fb = b / g.gather_rows;
-      gather_bf16(tm, a, b - fb * g.gather_rows, (int)fb, tile);
+      const int fb = (int)(b / g.gather_rows);
+      gather_bf16(tm, a, (int)(b - fb * g.gather_rows), fb * G_STEPS, tile);
       return;
     }
     b -= g.gather;
@@ -439,11 +480,12 @@ usaf_status restore(const Act8Args& a, void* x_out, void* x_perm, void* h, void*
                     cudaStream_t st) {
   CUtensorMap tm{};
   RestoreGrid g{};
-  const bool tiles = sizeof(T) == 2 && a.s.H % G_FEATURES == 0;
+  // (the tiles' vectors of codes are indexed in 32 bits)
+  const bool tiles = sizeof(T) == 2 && a.s.H % G_FEATURES == 0 && a.s.T * a.s.H < (int64_t(1) << 34);
   if (tiles) {
     if (!tcx::map_bf16_2d(&tm, x_perm, a.R_cap, a.s.H, 64, 64)) return USAF_ERR_CUDA;
     g.gather_rows = a.R_cap / G_ROWS;
-    g.gather = g.gather_rows * (a.s.H / G_FEATURES);
+    g.gather = g.gather_rows * ceil_div(a.s.H / G_FEATURES, G_STEPS);
   }
   g.row_segs = ceil_div(a.R_cap, 32 * Vec<T>::N);
   g.rows = g.row_segs * ceil_div(a.s.I, ROW_FEATURES);
@@ -454,11 +496,17 @@ usaf_status restore(const Act8Args& a, void* x_out, void* x_perm, void* h, void*
     USAF_TRACE("act8_restore", st);
     T *xo = static_cast<T*>(x_out), *ho = static_cast<T*>(h), *wo = static_cast<T*>(wa);
     if constexpr (sizeof(T) == 2) {
-      if (tiles)
+      if (tiles) {
+        // four blocks' tiles per SM; the rest of the shared memory stays L1
+        if (cudaFuncSetAttribute(act8_restore_kernel<T, true>,
+                                 cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 66) != cudaSuccess)
+          return USAF_ERR_CUDA;
         act8_restore_kernel<T, true><<<(unsigned)blocks, THREADS, G_SMEM, st>>>(tm, a, g, xo, ho,
                                                                                 wo);
-      else
+      } else {
         act8_restore_kernel<T, false><<<(unsigned)blocks, THREADS, 0, st>>>(tm, a, g, xo, ho, wo);
+      }
     } else {
       act8_restore_kernel<T, false><<<(unsigned)blocks, THREADS, 0, st>>>(tm, a, g, xo, ho, wo);
     }
