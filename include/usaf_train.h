@@ -88,8 +88,8 @@ usaf_status usaf_router_aux_bwd(int64_t T, int64_t E, int64_t k, const float* lo
  *   dev_status gets USAF_DEV_NONFINITE if a produced gradient is NaN/Inf, USAF_DEV_TIMEOUT if a
  *              tensor-core kernel gave up a wait
  * Sums are fp32 with dlogit carried exactly into g_router (three bf16 parts) and to 2^-16 into dx
- * of bf16 layers; their order is fixed. bf16 pointers x, dx_in, dx and w_router must be 16-byte
- * aligned (INVALID_ARG otherwise).
+ * of bf16 layers; their order is fixed. The workspace and, of bf16 layers, x, dx_in, dx and
+ * w_router must be 16-byte aligned (INVALID_ARG otherwise).
  * Limits: T >= 1, 1 <= E <= 1024, H >= 1, T < 2^31 - 65536, E*H < 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED (bf16 with H % 64 != 0), WORKSPACE, CUDA.
  * ------------------------------------------------------------------------------------------- */
@@ -118,9 +118,9 @@ usaf_status usaf_router_grad(int64_t T, int64_t E, int64_t H, usaf_dtype dtype,
  *   of that forward. dev_status gets USAF_DEV_NONFINITE if a block holds a NaN or infinity.
  * usaf_act8_restore: x_out [T,H] (or NULL), x_perm [H,R_cap], h [2I,R_cap], wa [I,R_cap] out, of
  *   dtype, with the same routing (topk_w, expert_offset, perm_tok, perm_slot are read). Padding
- *   rows come out 0; of the rows past expert_offset[E], x_perm's are 0 and those of h and wa may
- *   be left as they were, as after a forward.
- * All pointers of the store and the tensors must be 16-byte aligned.
+ *   rows come out 0 (in h and wa unless their block is NaN); of the rows past expert_offset[E],
+ *   x_perm's are 0 and those of h and wa may be left as they were, as after a forward.
+ * All pointers of the store and the tensors, perm_tok and perm_slot must be 16-byte aligned.
  * Any T, H, E, k, I of a valid shape, both dtypes. Errors: INVALID_ARG, CUDA.
  * ------------------------------------------------------------------------------------------- */
 #define USAF_ACT8_BLOCK 16

@@ -531,28 +531,51 @@ def reselect_carry(new_idx, old_idx, p_in, m_in, v_in, w_seg0, n_seg0, w_seg1, p
 ACT8_BLOCK = 16
 
 
-def _check_t(name: str, t, dtype, shape, device, optional=False, strided=False) -> None:
-    """The library reads and writes bare pointers: refuse a tensor of another dtype, shape, layout
-    or device before any launch. strided: the last axis contiguous, rows any distance apart."""
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+
+
+def _refuse(name, t, dtype, shape, dev):
+    """Say what is wrong with a tensor that _ok or _ok_rows turned down."""
     if t is None:
-        if optional:
-            return
         raise ValueError(f"{name} is required")
     if t.dtype != dtype or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected {list(shape)} {dtype}, got {list(t.shape)} {t.dtype}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: expected a tensor on the same CUDA device, got {t.device}")
-    if strided:
-        if t.shape[0] and (t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1]):
-            raise ValueError(f"{name}: rows must be contiguous and not overlap")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a tensor on CUDA device {max(dev, 0)}, got {t.device}")
+    raise ValueError(f"{name}: expected contiguous rows that do not overlap")
 
 
-def _ld(t) -> int:
-    """Distance between the rows of a [rows, n] tensor in elements (torch keeps any stride for one
-    row)."""
-    return max(int(t.stride(0)), t.shape[1])
+# The library reads and writes bare pointers, so tensors of another dtype, shape, layout or device
+# are refused before any launch. These run on every call of a step: attribute reads and no more.
+def _ok(name, t, dtype, shape, dev):
+    """The address of a contiguous tensor."""
+    if (t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0
+            or not t.is_contiguous()):
+        _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _opt(name, t, dtype, shape, dev):
+    return None if t is None else _ok(name, t, dtype, shape, dev)
+
+
+def _ok_rows(name, t, dtype, shape, dev):
+    """The address of a tensor whose rows may be a distance apart, and that distance (torch keeps
+    any stride for a single row)."""
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0:
+        _refuse(name, t, dtype, shape, dev)
+    ld, step = t.stride()
+    n = shape[1]
+    if (step != 1 and n > 1) or (ld < n and shape[0] > 1):
+        _refuse(name, t, dtype, shape, dev)
+    return t.data_ptr(), (ld if ld >= n else n)
+
+
+def _on(stream, dev):
+    """The stream handle: the device's current stream unless one is given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
 def router_aux_workspace_size(T: int, E: int, k: int, G: int = 1) -> int:
@@ -564,21 +587,22 @@ def router_aux_fwd(logits, topk_idx, k, count, prob_sum, n_tok, loss, coef_balan
     """usaf_router_aux_fwd: balance loss, z-loss and per-expert counts of logits [T,E] (rows may be
     a stride apart); count and prob_sum [G,E], n_tok [G], loss [3] = (total, balance, z)."""
     T, E = logits.shape
-    G, d = count.shape[0], logits.device
-    _check_t("logits", logits, torch.float32, (T, E), d, strided=True)
-    _check_t("topk_idx", topk_idx.reshape(-1), torch.int32, (T * k,), d)
-    _check_t("count", count, torch.int32, (G, E), d)
-    _check_t("prob_sum", prob_sum, torch.float32, (G, E), d)
-    _check_t("n_tok", n_tok, torch.int32, (G,), d)
-    _check_t("loss", loss, torch.float32, (3,), d)
-    _check_t("token_mask", token_mask, torch.uint8, (T,), d, optional=True)
-    _check_t("group_offset", group_offset, torch.int32, (G + 1,), d, optional=G == 1)
+    G, d = count.shape[0], logits.get_device()
+    if topk_idx.dim() == 2:
+        topk_idx = topk_idx.reshape(-1)
+    lp, ld = _ok_rows("logits", logits, _f32, (T, E), d)
+    ge = (G, E)
+    if group_offset is None and G != 1:
+        raise ValueError("group_offset is required")
     if ws is None:
-        ws = _ws(router_aux_workspace_size(T, E, k, G), d)
+        ws = _ws(router_aux_workspace_size(T, E, k, G), logits.device)
     _check("usaf_router_aux_fwd", lib().usaf_router_aux_fwd(
-        T, E, int(k), _ptr(logits), _ld(logits), _ptr(topk_idx), _ptr(token_mask),
-        _ptr(group_offset), G, float(coef_balance), float(coef_z), _ptr(count), _ptr(prob_sum),
-        _ptr(n_tok), _ptr(loss), _ptr(dev_status), _ptr(ws), ws.numel(), _stream(stream)))
+        T, E, k, lp, ld, _ok("topk_idx", topk_idx, _i32, (T * k,), d),
+        _opt("token_mask", token_mask, _u8, (T,), d),
+        _opt("group_offset", group_offset, _i32, (G + 1,), d), G, coef_balance, coef_z,
+        _ok("count", count, _i32, ge, d), _ok("prob_sum", prob_sum, _f32, ge, d),
+        _ok("n_tok", n_tok, _i32, (G,), d), _ok("loss", loss, _f32, (3,), d), _ptr(dev_status),
+        ws.data_ptr(), ws.numel(), _on(stream, d)))
 
 
 def router_aux_bwd(logits, k, count, n_tok, dlogit, coef_balance, coef_z, d_loss=None,
@@ -587,18 +611,17 @@ def router_aux_bwd(logits, k, count, n_tok, dlogit, coef_balance, coef_z, d_loss
     """usaf_router_aux_bwd: the gradient of the forward's loss[0] times d_loss ([1], None: 1) into
     dlogit [T,E] (accumulate = 1 adds); count and n_tok as the forward wrote them."""
     T, E = logits.shape
-    G, d = count.shape[0], logits.device
-    _check_t("logits", logits, torch.float32, (T, E), d, strided=True)
-    _check_t("dlogit", dlogit, torch.float32, (T, E), d, strided=True)
-    _check_t("count", count, torch.int32, (G, E), d)
-    _check_t("n_tok", n_tok, torch.int32, (G,), d)
-    _check_t("d_loss", d_loss, torch.float32, (1,), d, optional=True)
-    _check_t("token_mask", token_mask, torch.uint8, (T,), d, optional=True)
-    _check_t("group_offset", group_offset, torch.int32, (G + 1,), d, optional=G == 1)
+    G, d = count.shape[0], logits.get_device()
+    lp, ld = _ok_rows("logits", logits, _f32, (T, E), d)
+    op, ldo = _ok_rows("dlogit", dlogit, _f32, (T, E), d)
+    if group_offset is None and G != 1:
+        raise ValueError("group_offset is required")
     _check("usaf_router_aux_bwd", lib().usaf_router_aux_bwd(
-        T, E, int(k), _ptr(logits), _ld(logits), _ptr(token_mask), _ptr(group_offset), G,
-        float(coef_balance), float(coef_z), _ptr(count), _ptr(n_tok), _ptr(d_loss), _ptr(dlogit),
-        _ld(dlogit), int(accumulate), _ptr(dev_status), _stream(stream)))
+        T, E, k, lp, ld, _opt("token_mask", token_mask, _u8, (T,), d),
+        _opt("group_offset", group_offset, _i32, (G + 1,), d), G, coef_balance, coef_z,
+        _ok("count", count, _i32, (G, E), d), _ok("n_tok", n_tok, _i32, (G,), d),
+        _opt("d_loss", d_loss, _f32, (1,), d), op, ldo, int(accumulate), _ptr(dev_status),
+        _on(stream, d)))
 
 
 def router_grad_workspace_size(T: int, E: int, H: int, dtype) -> int:
@@ -613,22 +636,18 @@ def router_grad(dlogit, x, w_router, g_router=None, g_in=None, dx=None, dx_in=No
     where its output is given (g_in / dx_in None: zero; they may be the outputs themselves)."""
     T, E = dlogit.shape
     ref = x if x is not None else dx
-    if ref is None:
+    if ref is None or (x is None and g_router is not None):
         raise ValueError("x is required")
-    H, d = ref.shape[1], dlogit.device
-    _check_t("dlogit", dlogit, torch.float32, (T, E), d, strided=True)
-    _check_t("x", x, ref.dtype, (T, H), d, optional=g_router is None)
-    _check_t("w_router", w_router, torch.float32, (E, H), d, optional=dx is None)
-    for name, t in (("g_router", g_router), ("g_in", g_in)):
-        _check_t(name, t, torch.float32, (E, H), d, optional=True)
-    for name, t in (("dx", dx), ("dx_in", dx_in)):
-        _check_t(name, t, ref.dtype, (T, H), d, optional=True)
+    H, d, dt = ref.shape[1], dlogit.get_device(), ref.dtype
+    dp, ld = _ok_rows("dlogit", dlogit, _f32, (T, E), d)
+    th, eh = (T, H), (E, H)
     if ws is None:
-        ws = _ws(router_grad_workspace_size(T, E, H, ref.dtype), d)
+        ws = _ws(router_grad_workspace_size(T, E, H, dt), dlogit.device)
     _check("usaf_router_grad", lib().usaf_router_grad(
-        T, E, H, _dt(ref), _ptr(dlogit), _ld(dlogit), _ptr(x), _ptr(w_router), _ptr(g_in),
-        _ptr(g_router), _ptr(dx_in), _ptr(dx), _ptr(dev_status), _ptr(ws), ws.numel(),
-        _stream(stream)))
+        T, E, H, _dt(ref), dp, ld, _opt("x", x, dt, th, d),
+        _opt("w_router", w_router, _f32, eh, d), _opt("g_in", g_in, _f32, eh, d),
+        _opt("g_router", g_router, _f32, eh, d), _opt("dx_in", dx_in, dt, th, d),
+        _opt("dx", dx, dt, th, d), _ptr(dev_status), ws.data_ptr(), ws.numel(), _on(stream, d)))
 
 
 @dataclass
@@ -655,42 +674,35 @@ class ActStore8:
     def nbytes(self) -> int:
         return sum(t.numel() for t in (self.x_code, self.x_exp, self.h_code, self.h_exp))
 
-    def check(self, s: Shape, device) -> None:
-        sh = ActStore8.shapes(s)
-        _check_t("x_code", self.x_code, torch.int8, sh[0], device)
-        _check_t("x_exp", self.x_exp, torch.uint8, sh[1], device)
-        _check_t("h_code", self.h_code, torch.int8, sh[2], device)
-        _check_t("h_exp", self.h_exp, torch.uint8, sh[3], device)
+    def ptrs(self, sh: tuple, dev: int) -> tuple:
+        """The addresses, checked against the shapes of ActStore8.shapes."""
+        return (_ok("x_code", self.x_code, torch.int8, sh[0], dev),
+                _ok("x_exp", self.x_exp, _u8, sh[1], dev),
+                _ok("h_code", self.h_code, torch.int8, sh[2], dev),
+                _ok("h_exp", self.h_exp, _u8, sh[3], dev))
 
 
 def act8_save(s: Shape, x, h, rt: Routing, store: ActStore8, dev_status=None, stream=None):
     """usaf_act8_save: x [T,H] and h [2I,R_cap] of a forward into the store."""
-    d = x.device
-    _check_t("x", x, x.dtype, (s.T, s.H), d)
-    _check_t("h", h, x.dtype, ActStore8.shapes(s)[2], d)
-    store.check(s, d)
+    d, sh = x.get_device(), ActStore8.shapes(s)
+    xp, hp = _ok("x", x, x.dtype, sh[0], d), _ok("h", h, x.dtype, sh[2], d)
     r = rt.c()
     _check("usaf_act8_save", lib().usaf_act8_save(
-        ctypes.byref(s), _dt(x), _ptr(x), _ptr(h), ctypes.byref(r), _ptr(store.x_code),
-        _ptr(store.x_exp), _ptr(store.h_code), _ptr(store.h_exp), _ptr(dev_status),
-        _stream(stream)))
+        ctypes.byref(s), _dt(x), xp, hp, ctypes.byref(r), *store.ptrs(sh, d), _ptr(dev_status),
+        _on(stream, d)))
 
 
 def act8_restore(s: Shape, store: ActStore8, rt: Routing, x_perm, h, wa, x=None, stream=None):
     """usaf_act8_restore: what the backward reads (x_perm, h, wa; x too unless None) from the
     store and the routing of that forward."""
-    d, dt = h.device, h.dtype
-    cap = routed_rows_capacity(s)
-    store.check(s, d)
-    _check_t("x", x, dt, (s.T, s.H), d, optional=True)
-    _check_t("x_perm", x_perm, dt, (s.H, cap), d)
-    _check_t("h", h, dt, (2 * s.I, cap), d)
-    _check_t("wa", wa, dt, (s.I, cap), d)
+    d, dt, sh = h.get_device(), h.dtype, ActStore8.shapes(s)
+    cap = sh[2][1]
+    ptrs = store.ptrs(sh, d)
     r = rt.c()
     _check("usaf_act8_restore", lib().usaf_act8_restore(
-        ctypes.byref(s), _dt(h), _ptr(store.x_code), _ptr(store.x_exp), _ptr(store.h_code),
-        _ptr(store.h_exp), ctypes.byref(r), _ptr(x), _ptr(x_perm), _ptr(h), _ptr(wa),
-        _stream(stream)))
+        ctypes.byref(s), _dt(h), *ptrs, ctypes.byref(r), _opt("x", x, dt, sh[0], d),
+        _ok("x_perm", x_perm, dt, (s.H, cap), d), _ok("h", h, dt, sh[2], d),
+        _ok("wa", wa, dt, (s.I, cap), d), _on(stream, d)))
 
 
 def trace_enable(on: bool) -> None:

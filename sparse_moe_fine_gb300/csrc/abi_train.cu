@@ -130,6 +130,7 @@ usaf_status usaf_router_grad(int64_t T, int64_t E, int64_t H, usaf_dtype dtype,
       return USAF_ERR_INVALID_ARG;
   }
   if (!ws || ws_bytes < usaf_router_grad_workspace_size(T, E, H, dtype)) return USAF_ERR_WORKSPACE;
+  if (!aligned16(ws)) return USAF_ERR_INVALID_ARG;
   RouterGradArgs a{T, E, H, ld_dlogit, dtype, dlogit, x, w_router, g_in, g_router, dx_in, dx,
                    dev_status};
   Carver c(ws);
@@ -155,7 +156,8 @@ usaf_status usaf_act8_restore(const usaf_moe_shape* shape, usaf_dtype dtype, con
   USAF_TRY(fill_act8(a, shape, dtype, x_code, x_exp, h_code, h_exp, rt));
   if (!x_perm || !h || !wa || !rt->topk_w || !rt->perm_tok || !rt->perm_slot)
     return USAF_ERR_INVALID_ARG;
-  if (!aligned16(x_out) || !aligned16(x_perm) || !aligned16(h) || !aligned16(wa))
+  if (!aligned16(x_out) || !aligned16(x_perm) || !aligned16(h) || !aligned16(wa) ||
+      !aligned16(rt->perm_tok) || !aligned16(rt->perm_slot))
     return USAF_ERR_INVALID_ARG;
   return act8_restore_launch(a, x_out, x_perm, h, wa, static_cast<cudaStream_t>(stream));
 }

@@ -4,8 +4,6 @@
 // A row of E logits is held by LPR neighbouring lanes, NV values each (expert sub + LPR i), so a
 // softmax is one read of the row, two butterflies and no shared memory; routers of at most 16
 // experts put several rows into a warp.
-#include <cooperative_groups.h>
-
 #include <type_traits>
 
 #include "train.cuh"
@@ -16,8 +14,11 @@ namespace {
 
 constexpr int AUX_WARPS = 8;
 constexpr int AUX_THREADS = 32 * AUX_WARPS;
-constexpr int FIN_CTAS = 8;
-constexpr int FIN_THREADS = 512;
+constexpr int FIN_WARPS = 32;   // slot lanes of a final block, 32 experts wide
+constexpr int FIN_THREADS = 32 * FIN_WARPS;
+// Rows a warp has in flight: enough loads to cover DRAM's latency, 16 values a lane at most.
+template <int NV>
+constexpr int ROWS = NV <= 4 ? 4 : (NV <= 8 ? 2 : 1);
 
 struct AuxParams {
   int64_t T, ld;
@@ -143,13 +144,14 @@ __global__ void __launch_bounds__(AUX_THREADS)
   __shared__ float s_z[AUX_WARPS];
   __shared__ int s_n[AUX_WARPS];
   __shared__ double s_red[AUX_THREADS];
-  constexpr int RPW = 32 / LPR;
+  constexpr int RPW = 32 / LPR, U = ROWS<NV>, PRE = 4;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane % LPR, rw = lane / LPR;
   const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   check_offsets(p, (int64_t)blockIdx.x * blockDim.x + threadIdx.x,
                 (int64_t)gridDim.x * blockDim.x);
   for (int e = threadIdx.x; e < p.E; e += AUX_THREADS) s_cnt[e] = 0;
+  if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *w.arrived = 0;  // for the final kernel
   if constexpr (ONE) {
     for (int64_t i = threadIdx.x; i < (int64_t)p.G * p.E; i += AUX_THREADS) {
       count_out[i] = 0;
@@ -171,23 +173,36 @@ __global__ void __launch_bounds__(AUX_THREADS)
     int64_t te = min(t1, clamp_off(p, g + 1));
     if (te <= t) te = t + 1;  // only where the offsets decrease
     __syncthreads();  // the last segment's counts are out; ONE: the zeroed outputs too
+    // the segment's first expert indices, on their way while the rows are read
+    const int64_t q0 = t * p.k + threadIdx.x, q1 = te * p.k;
+    int ids[PRE];
+#pragma unroll
+    for (int u = 0; u < PRE; ++u)
+      ids[u] = q0 + u * AUX_THREADS < q1 ? p.topk[q0 + u * AUX_THREADS] : 0;
     float acc[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) acc[i] = 0.f;
     float z = 0.f;
     int n = 0;
-    for (int64_t base = t + wid * RPW; base < te; base += AUX_WARPS * RPW) {
-      const int64_t tok = base + rw;
-      const bool in = tok < te && (!p.mask || p.mask[tok] != 0);
-      float v[NV], lse;
-      load_row<LPR, NV>(p, tok, in, sub, v);
-      const bool alive = row_softmax<LPR, NV>(v, lse);
+    for (int64_t base = t + wid * RPW; base < te; base += AUX_WARPS * RPW * U) {
+      float v[U][NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) acc[i] += v[i];
-      if (sub == 0) {
-        z += lse * lse;
-        n += alive ? 1 : 0;
-        if (tok < te) s_live[tok - t0] = alive ? 1 : 0;
+      for (int u = 0; u < U; ++u) {
+        const int64_t tok = base + u * AUX_WARPS * RPW + rw;
+        load_row<LPR, NV>(p, tok, tok < te && (!p.mask || p.mask[tok] != 0), sub, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t tok = base + u * AUX_WARPS * RPW + rw;
+        float lse;
+        const bool alive = row_softmax<LPR, NV>(v[u], lse);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) acc[i] += v[u][i];
+        if (sub == 0) {
+          z += lse * lse;
+          n += alive ? 1 : 0;
+          if (tok < te) s_live[tok - t0] = alive ? 1 : 0;
+        }
       }
     }
 #pragma unroll
@@ -210,13 +225,15 @@ __global__ void __launch_bounds__(AUX_THREADS)
     }
     __syncthreads();
     // the experts that the segment's live tokens went to
-    const int64_t q1 = te * p.k;
-    for (int64_t q = t * p.k + threadIdx.x; q < q1; q += AUX_THREADS) {
-      if (!s_live[q / p.k - t0]) continue;
-      const int e = p.topk[q];
+    auto add = [&](int64_t q, int e) {
+      if (!s_live[(int)(q - t0 * p.k) / p.k]) return;
       if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
       else badidx = true;
-    }
+    };
+#pragma unroll
+    for (int u = 0; u < PRE; ++u)
+      if (q0 + u * AUX_THREADS < q1) add(q0 + u * AUX_THREADS, ids[u]);
+    for (int64_t q = q0 + PRE * AUX_THREADS; q < q1; q += AUX_THREADS) add(q, p.topk[q]);
     __syncthreads();
     const int64_t slot = ONE ? g : (int64_t)blockIdx.x + g;
     float* po = ONE ? prob_out : w.prob;
@@ -261,111 +278,96 @@ __global__ void __launch_bounds__(AUX_THREADS)
   }
 }
 
-// Sums the chunks' partials into the groups' outputs and forms the loss: one cluster, CTA r the
-// experts [r w, (r + 1) w), w = ceil(E / FIN_CTAS). A CTA's threads are (group lane, slot lane, expert): `sl`
-// slot lanes share a group's chunks and are added by a tree.
-__global__ void __cluster_dims__(FIN_CTAS, 1, 1) __launch_bounds__(FIN_THREADS)
-    aux_final_kernel(const AuxParams p, AuxWs w, int el, int sl, int32_t* __restrict__ count,
+// Sums the chunks' partials of 32 experts of a group: lanes are experts, warps share the chunks.
+// The block that arrives last (a counter that the partials' kernel cleared) adds the blocks'
+// shares of the loss in their order.
+__global__ void __launch_bounds__(FIN_THREADS)
+    aux_final_kernel(const AuxParams p, AuxWs w, int nb, int32_t* __restrict__ count,
                      float* __restrict__ prob, int32_t* __restrict__ n_tok,
                      float* __restrict__ loss) {
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();
-  __shared__ float s_p[FIN_THREADS], s_z[FIN_THREADS];
-  __shared__ int32_t s_c[FIN_THREADS], s_n[FIN_THREADS];
-  __shared__ double s_bal;
-  const int rank = (int)cluster.block_rank();
-  const int tx = threadIdx.x % el, ty = threadIdx.x / el;
-  const int ls = ty % sl, lg = ty / sl, gl = FIN_THREADS / el / sl;
-  const int wd = (p.E + FIN_CTAS - 1) / FIN_CTAS;
-  const int e = rank * wd + tx;
-  const bool ev = tx < wd && e < p.E;
-  double bal = 0.0;
-  float z = 0.f;
-  int64_t n_all = 0;
-  for (int g0 = 0; g0 < p.G; g0 += gl) {
-    const int g = g0 + lg;
-    float a = 0.f, zz = 0.f;
-    int32_t c = 0, n = 0;
-    if (g < p.G) {
-      const int64_t o0 = clamp_off(p, g), o1 = clamp_off(p, g + 1);
-      if (o1 > o0) {
-        const int64_t c1 = (o1 - 1) / p.chunk;
-        for (int64_t ch = o0 / p.chunk + ls; ch <= c1; ch += sl) {
-          const int64_t slot = ch + g;
-          if (ev) {
-            a += w.prob[slot * p.E + e];
-            c += w.count[slot * p.E + e];
-          }
-          if (tx == 0) {
-            n += w.n[slot];
-            zz += w.z[slot];
-          }
-        }
+  __shared__ float s_p[FIN_WARPS][33], s_z[FIN_WARPS];
+  __shared__ int32_t s_c[FIN_WARPS][33], s_n[FIN_WARPS];
+  __shared__ bool s_last;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int g = blockIdx.x / nb, eb = blockIdx.x % nb, e = eb * 32 + lane;
+  float a = 0.f, z = 0.f;
+  int32_t c = 0, n = 0;
+  const int64_t o0 = clamp_off(p, g), o1 = clamp_off(p, g + 1);
+  if (o1 > o0) {
+    const int64_t ch1 = (o1 - 1) / p.chunk;
+#pragma unroll 8
+    for (int64_t ch = o0 / p.chunk + wid; ch <= ch1; ch += FIN_WARPS) {
+      const int64_t slot = ch + g;
+      if (e < p.E) {
+        a += w.prob[slot * p.E + e];
+        c += w.count[slot * p.E + e];
+      }
+      if (lane == 0) {
+        n += w.n[slot];
+        z += w.z[slot];
       }
     }
-    s_p[threadIdx.x] = a;
-    s_c[threadIdx.x] = c;
-    s_n[threadIdx.x] = n;
-    s_z[threadIdx.x] = zz;
-    __syncthreads();
-    for (int h = sl / 2; h; h >>= 1) {
-      if (ls < h) {
-        s_p[threadIdx.x] += s_p[threadIdx.x + h * el];
-        s_c[threadIdx.x] += s_c[threadIdx.x + h * el];
-        s_n[threadIdx.x] += s_n[threadIdx.x + h * el];
-        s_z[threadIdx.x] += s_z[threadIdx.x + h * el];
-      }
-      __syncthreads();
-    }
-    if (ls == 0 && g < p.G) {
-      const int ng = s_n[threadIdx.x - tx];
-      if (ev) {
-        const float P = s_p[threadIdx.x];
-        const int32_t cc = s_c[threadIdx.x];
-        prob[(int64_t)g * p.E + e] = P;
-        count[(int64_t)g * p.E + e] = cc;
-        if (ng > 0) bal += (double)((float)cc * P) / ng;
-      }
-      if (tx == 0) {
-        z += s_z[threadIdx.x];
-        n_all += ng;
-        if (rank == 0) n_tok[g] = ng;
-      }
-    }
-    __syncthreads();
   }
-  // the block's sums in a fixed order: warps by butterfly, then the warps in turn
-  for (int o = 16; o; o >>= 1) {
-    bal += __shfl_xor_sync(0xffffffffu, bal, o);
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-    n_all += __shfl_xor_sync(0xffffffffu, n_all, o);
-  }
-  __shared__ double r_bal[FIN_THREADS / 32];
-  __shared__ float r_z[FIN_THREADS / 32];
-  __shared__ int64_t r_n[FIN_THREADS / 32];
-  if ((threadIdx.x & 31) == 0) {
-    r_bal[threadIdx.x >> 5] = bal;
-    r_z[threadIdx.x >> 5] = z;
-    r_n[threadIdx.x >> 5] = n_all;
+  s_p[wid][lane] = a;
+  s_c[wid][lane] = c;
+  if (lane == 0) {
+    s_n[wid] = n;
+    s_z[wid] = z;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double b = 0.0;
-    for (int i = 0; i < FIN_THREADS / 32; ++i) b += r_bal[i];
-    s_bal = b;
-  }
-  cluster.sync();
-  if (rank == 0 && threadIdx.x == 0) {
-    double b = 0.0, zs = 0.0;
-    int64_t n = 0;
-    for (int r = 0; r < FIN_CTAS; ++r) b += *cluster.map_shared_rank(&s_bal, r);
-    for (int i = 0; i < FIN_THREADS / 32; ++i) {
-      zs += r_z[i];
-      n += r_n[i];
+  if (wid == 0) {
+    a = z = 0.f;
+    c = n = 0;
+#pragma unroll 8
+    for (int u = 0; u < FIN_WARPS; ++u) {
+      a += s_p[u][lane];
+      c += s_c[u][lane];
+      n += s_n[u];
+      z += s_z[u];
     }
-    write_loss(p, b, zs, n, loss);
+    double bal = 0.0;
+    if (e < p.E) {
+      prob[(int64_t)g * p.E + e] = a;
+      count[(int64_t)g * p.E + e] = c;
+      if (n > 0) bal = (double)((float)c * a) / n;
+    }
+    for (int o = 16; o; o >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, o);
+    if (lane == 0) {
+      w.bal[blockIdx.x] = bal;
+      if (eb == 0) {
+        n_tok[g] = n;
+        w.group_z[g] = z;
+      }
+      __threadfence();
+      s_last = atomicAdd(w.arrived, 1u) == gridDim.x - 1;
+    }
   }
-  cluster.sync();  // no CTA leaves while its shared memory may be read
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  // fixed order: thread t its share of the blocks and groups, then a tree
+  __shared__ double r_b[FIN_THREADS], r_z[FIN_THREADS];
+  __shared__ int64_t r_n[FIN_THREADS];
+  double sb = 0.0, sz = 0.0;
+  int64_t sn = 0;
+  for (int64_t i = threadIdx.x; i < gridDim.x; i += FIN_THREADS) sb += __ldcg(w.bal + i);
+  for (int i = threadIdx.x; i < p.G; i += FIN_THREADS) {
+    sz += __ldcg(w.group_z + i);
+    sn += __ldcg(n_tok + i);
+  }
+  r_b[threadIdx.x] = sb;
+  r_z[threadIdx.x] = sz;
+  r_n[threadIdx.x] = sn;
+  __syncthreads();
+  for (int h = FIN_THREADS / 2; h; h >>= 1) {
+    if (threadIdx.x < h) {
+      r_b[threadIdx.x] += r_b[threadIdx.x + h];
+      r_z[threadIdx.x] += r_z[threadIdx.x + h];
+      r_n[threadIdx.x] += r_n[threadIdx.x + h];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) write_loss(p, r_b[0], r_z[0], r_n[0], loss);
 }
 
 // The gradient: each row is read once, its group's counts stay in registers while the group lasts.
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(AUX_THREADS)
                    const int32_t* __restrict__ n_tok, const float* __restrict__ d_loss, float* out,
                    int64_t ld_out, int accumulate, int rows_per_lane) {
   __shared__ int64_t s_n[AUX_WARPS];
-  constexpr int RPW = 32 / LPR;
+  constexpr int RPW = 32 / LPR, U = ROWS<NV>;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane % LPR, rw = lane / LPR;
   check_offsets(p, (int64_t)blockIdx.x * blockDim.x + threadIdx.x,
@@ -398,42 +400,54 @@ __global__ void __launch_bounds__(AUX_THREADS)
 #pragma unroll
   for (int i = 0; i < NV; ++i) c[i] = 0.f;
   bool bad = false;
-  for (int r = 0; r < rows_per_lane; ++r) {
-    if (first + r * RPW >= p.T) break;
-    const int64_t tok = first + r * RPW + rw;
-    bool in = tok < p.T;
-    if (in && (cur == -2 || tok >= cur_end)) {
-      cur = group_of(p, tok);
-      cur_end = cur >= 0 ? clamp_off(p, cur + 1) : (tok < clamp_off(p, 0) ? clamp_off(p, 0) : p.T);
-      const int ng = cur >= 0 ? n_tok[cur] : 0;
-      cg = p.coef_b != 0.f && ng > 0 ? up * p.coef_b * p.share * inv_n / (float)ng : 0.f;
-      if (cur >= 0) {
+  for (int r0 = 0; r0 < rows_per_lane; r0 += U) {
+    if (first + r0 * RPW >= p.T) break;
+    float v[U][NV];
+    bool in_group[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t tok = first + (r0 + u) * RPW + rw;
+      in_group[u] = r0 + u < rows_per_lane && tok < p.T && (!p.mask || p.mask[tok] != 0);
+      load_row<LPR, NV>(p, tok, in_group[u], sub, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t tok = first + (r0 + u) * RPW + rw;
+      const bool in = r0 + u < rows_per_lane && tok < p.T;
+      if (in && (cur == -2 || tok >= cur_end)) {
+        cur = group_of(p, tok);
+        cur_end = cur >= 0 ? clamp_off(p, cur + 1) : (tok < clamp_off(p, 0) ? clamp_off(p, 0) : p.T);
+        const int ng = cur >= 0 ? n_tok[cur] : 0;
+        cg = p.coef_b != 0.f && ng > 0 ? up * p.coef_b * p.share * inv_n / (float)ng : 0.f;
+        if (cur >= 0) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int e = sub + LPR * i;
+            c[i] = e < p.E ? (float)count[(int64_t)cur * p.E + e] : 0.f;
+          }
+        }
+      }
+      if (cur < 0)  // a token of no group takes no part
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[u][i] = -INFINITY;
+      float lse;
+      row_softmax<LPR, NV>(v[u], lse);
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s = fmaf(v[u][i], c[i], s);
+      s = row_sum<LPR>(s);
+      const float zt = zc * lse;
+      if (in) {
+        float* o = out + tok * ld_out;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int e = sub + LPR * i;
-          c[i] = e < p.E ? (float)count[(int64_t)cur * p.E + e] : 0.f;
-        }
-      }
-    }
-    const bool row_in = in && cur >= 0 && (!p.mask || p.mask[tok] != 0);
-    float v[NV], lse;
-    load_row<LPR, NV>(p, tok, row_in, sub, v);
-    row_softmax<LPR, NV>(v, lse);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s = fmaf(v[i], c[i], s);
-    s = row_sum<LPR>(s);
-    const float zt = zc * lse;
-    if (in) {
-      float* o = out + tok * ld_out;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = sub + LPR * i;
-        if (e < p.E) {
-          float d = v[i] * fmaf(cg, c[i] - s, zt);
-          if (accumulate) d += o[e];
-          o[e] = d;
-          bad |= !finite_f(d);
+          if (e < p.E) {
+            float d = v[u][i] * fmaf(cg, c[i] - s, zt);
+            if (accumulate) d += o[e];
+            o[e] = d;
+            bad |= !finite_f(d);
+          }
         }
       }
     }
@@ -448,7 +462,7 @@ AuxParams make_params(const AuxArgs& a) {
   p.E = a.E;
   p.k = a.k;
   p.G = (int)a.G;
-  p.chunk = (int)aux_chunk_tokens(a.T);
+  p.chunk = (int)aux_chunk_tokens(a.T, a.E);
   p.nchunks = (int)ceil_div(a.T, p.chunk);
   p.logits = a.logits;
   p.topk = a.topk_idx;
@@ -479,19 +493,24 @@ usaf_status by_width(int E, F f) {
 
 }  // namespace
 
-// Tokens of a chunk: eight warps of the block that owns it, at most about two chunks per SM.
-int64_t aux_chunk_tokens(int64_t T) {
-  const int64_t per = ceil_div(T, 2 * 152);
-  const int64_t c = round_up(per, 32);
+// Tokens of a chunk. A batch of at most eight rows a warp is one chunk, whose block forms the outputs
+// itself (one launch); longer ones have about two chunks per SM.
+int64_t aux_chunk_tokens(int64_t T, int64_t E) {
+  const int64_t rows = E <= 8 ? 4 : (E <= 16 ? 2 : 1);  // of a warp at a time
+  if (T <= 8 * AUX_WARPS * rows) return T;
+  const int64_t c = round_up(ceil_div(T, 2 * 152), 32);
   return c < 32 ? 32 : c;
 }
 
 void aux_ws_layout(int64_t T, int64_t E, int64_t G, Carver& c, AuxWs& w) {
-  const int64_t slots = ceil_div(T, aux_chunk_tokens(T)) + G - 1;
+  const int64_t slots = ceil_div(T, aux_chunk_tokens(T, E)) + G - 1;
   w.prob = c.take<float>(slots * E);
   w.count = c.take<int32_t>(slots * E);
   w.n = c.take<int32_t>(slots);
   w.z = c.take<float>(slots);
+  w.bal = c.take<double>(G * ceil_div(E, 32));
+  w.group_z = c.take<float>(G);
+  w.arrived = c.take<uint32_t>(1);
 }
 
 usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, int32_t* n_tok,
@@ -515,13 +534,9 @@ usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, in
   }));
   if (one) return USAF_OK;
   USAF_TRACE("router_aux_final", st);
-  const int wd = (a.E + FIN_CTAS - 1) / FIN_CTAS;
-  int el = 1;
-  while (el < wd) el *= 2;
-  int sl = 1;
-  const int64_t per_group = ceil_div(p.nchunks, a.G) + 1;
-  while (sl * 2 <= FIN_THREADS / el && sl < per_group) sl *= 2;
-  aux_final_kernel<<<FIN_CTAS, FIN_THREADS, 0, st>>>(p, w, el, sl, count, prob_sum, n_tok, loss);
+  const int nb = (int)ceil_div(a.E, 32);  // blocks of a group
+  aux_final_kernel<<<(unsigned)(nb * a.G), FIN_THREADS, 0, st>>>(p, w, nb, count, prob_sum, n_tok,
+                                                                 loss);
   USAF_CHECK_LAUNCH();
   return USAF_OK;
 }
@@ -536,7 +551,7 @@ usaf_status aux_bwd_launch(const AuxArgs& a, const int32_t* count, const int32_t
     // rows per lane group: enough blocks for every SM first, then rows that share a count load
     const int64_t lanes = (int64_t)AUX_WARPS * RPW;
     int rows = 1;
-    while (rows < 8 && ceil_div(a.T, lanes * rows * 2) >= 4 * 152) rows *= 2;
+    while (rows < 16 && ceil_div(a.T, lanes * rows * 2) >= 2 * 152) rows *= 2;
     const unsigned grid = (unsigned)ceil_div(a.T, lanes * rows);
     aux_bwd_kernel<lpr.value, nv.value><<<grid, AUX_THREADS, 0, st>>>(
         p, count, n_tok, d_loss, dlogit, ld_out, accumulate, rows);

@@ -24,8 +24,11 @@ struct AuxWs {
   int32_t* count;
   int32_t* n;  // [slots]
   float* z;
+  double* bal;        // [G][ceil(E / 32)] shares of the balance sum
+  float* group_z;     // [G]
+  uint32_t* arrived;  // blocks of the final kernel that are done
 };
-int64_t aux_chunk_tokens(int64_t T);  // tokens of a chunk
+int64_t aux_chunk_tokens(int64_t T, int64_t E);  // tokens of a chunk
 void aux_ws_layout(int64_t T, int64_t E, int64_t G, Carver& c, AuxWs& w);
 usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, int32_t* n_tok,
                            float* loss, const AuxWs& w, cudaStream_t st);

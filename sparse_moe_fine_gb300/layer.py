@@ -11,6 +11,13 @@ Data parallel (the README's DataParallel mode): every rank holds the same weight
 and runs the step on its own tokens; before the optimizer, one all-reduce sums the compact
 gradients (K active expert entries and the E*H router entries) and one takes the maximum of the
 status words, so every replica applies the same update or skips the same step.
+
+Two additions to the step, both off unless asked for (see include/usaf_train.h):
+- a load-balance loss and a z-loss on the router's logits (balance_coef, z_coef): their gradient
+  joins the router's gradient and dx. Under data parallelism each rank adds the loss of its own
+  tokens, and the ranks' gradients are summed like the rest;
+- activations in 8 bits (save_act8 / restore_act8) between a forward and its backward, so that
+  layers can share the buffers a forward leaves (share_activations; StackTrainer(act8=True)).
 """
 from __future__ import annotations
 
@@ -50,7 +57,7 @@ def allreduce_dense_grad(g_dense, group=None):
 class MoELayer:
     def __init__(self, T, H, E, k, I, w_gate_up, w_down, w_router, act_idx, lr=1e-4,
                  betas=(0.9, 0.999), eps=1e-8, renorm=1, device="cuda", group=None,
-                 dense_density=0.015):
+                 dense_density=0.015, balance_coef=0.0, z_coef=0.0):
         self.dev = torch.device(device)
         self.s = B.shape(T, H, E, k, I)
         self.T, self.H, self.E, self.k, self.I = T, H, E, k, I
@@ -100,6 +107,11 @@ class MoELayer:
                                     device=d)
         self.ws_fwd = torch.empty(B.moe_fwd_workspace_size(self.s, self.dt), dtype=torch.uint8,
                                   device=d)
+        # auxiliary losses of the router
+        self.balance_coef, self.z_coef = float(balance_coef), float(z_coef)
+        self.aux = self.balance_coef != 0.0 or self.z_coef != 0.0
+        self._graphs = {}
+        self.set_sequences()
         # router SparseAdam state (dense over all E*H entries)
         self.r_p = self.w_router.reshape(-1).clone()
         self.r_m = torch.zeros_like(self.r_p)
@@ -145,6 +157,84 @@ class MoELayer:
                                   dtype=torch.uint8, device=self.dev)
         self._graphs = {}  # captured steps hold the old active set's pointers
 
+    # ------------------------------------------------------------------ auxiliary losses
+    def set_sequences(self, group_offset=None, token_mask=None):
+        """The sequences that the auxiliary losses see in the next batches: group_offset [G+1] int32
+        (first token of each packed sequence; None: the batch is one) and token_mask [T] uint8 (0:
+        a padding token that takes no part; None: every token does). The tensors are read by every
+        later step, so a caller that changes only their contents may write into them. With the
+        losses on: aux_count and aux_prob [G,E], aux_n [G] and aux_loss [3] (total, balance, z) hold
+        the last forward's values."""
+        if not self.aux:
+            if group_offset is not None or token_mask is not None:
+                raise ValueError("sequences are only for the auxiliary losses, which are off")
+            return
+        d, T, E = self.dev, self.T, self.E
+        for name, t, dt in (("group_offset", group_offset, torch.int32),
+                            ("token_mask", token_mask, torch.uint8)):
+            if t is None:
+                continue
+            if t.dtype != dt or not t.is_cuda or not t.is_contiguous() or t.dim() != 1:
+                raise ValueError(f"{name}: expected a contiguous one-dimensional CUDA {dt} tensor")
+        if token_mask is not None and token_mask.numel() != T:
+            raise ValueError(f"token_mask: expected {T} entries, got {token_mask.numel()}")
+        if group_offset is not None and group_offset.numel() < 2:
+            raise ValueError("group_offset needs at least two entries")
+        G = 1 if group_offset is None else group_offset.numel() - 1
+        self.group_offset, self.token_mask = group_offset, token_mask
+        self.aux_count = torch.zeros(G, E, dtype=torch.int32, device=d)
+        self.aux_prob = torch.zeros(G, E, device=d)
+        self.aux_n = torch.zeros(G, dtype=torch.int32, device=d)
+        self.aux_loss = torch.zeros(3, device=d)
+        self.dlogit_aux = torch.empty(T, E, device=d)
+        self.ws_aux = torch.empty(B.router_aux_workspace_size(T, E, self.k, G), dtype=torch.uint8,
+                                  device=d)
+        self.ws_rgrad = torch.empty(B.router_grad_workspace_size(T, E, self.H, self.dtype),
+                                    dtype=torch.uint8, device=d)
+        self._graphs = {}  # captured steps hold the old buffers' pointers
+
+    def _aux_forward(self, stream=None, dev_status=None):
+        B.router_aux_fwd(self.logits, self.rt.topk_idx, self.k, self.aux_count, self.aux_prob,
+                         self.aux_n, self.aux_loss, self.balance_coef, self.z_coef,
+                         token_mask=self.token_mask, group_offset=self.group_offset,
+                         dev_status=dev_status, ws=self.ws_aux, stream=stream)
+
+    def _aux_backward(self, x, dx, stream=None, dev_status=None):
+        """Adds the losses' gradient to g_router and, unless None, dx."""
+        B.router_aux_bwd(self.logits, self.k, self.aux_count, self.aux_n, self.dlogit_aux,
+                         self.balance_coef, self.z_coef, token_mask=self.token_mask,
+                         group_offset=self.group_offset, dev_status=dev_status, stream=stream)
+        B.router_grad(self.dlogit_aux, x, self.w_router, g_router=self.g_router,
+                      g_in=self.g_router, dx=dx, dx_in=dx, dev_status=dev_status,
+                      ws=self.ws_rgrad, stream=stream)
+
+    # ------------------------------------------------------------------ activations in 8 bits
+    def save_act8(self, x, store=None, stream=None):
+        """The last forward's activations as an 8-bit store (a new one unless `store` is given): x
+        and h; x_perm and wa are formed again by restore_act8. x_perm, h and wa may then be
+        overwritten until the restore; the routing tables stay as they are."""
+        self._check_tokens(x=x)
+        if store is None:
+            store = B.ActStore8.empty(self.s, self.dev)
+        B.act8_save(self.s, x, self.h, self.rt, store, dev_status=self.status, stream=stream)
+        return store
+
+    def restore_act8(self, store, x, stream=None):
+        """What the backward reads, from the store of this layer's forward: x_perm, h and wa in the
+        layer's buffers, the layer's input in x [T,H]. Returns x."""
+        self._check_tokens(x=x)
+        B.act8_restore(self.s, store, self.rt, self.x_perm, self.h, self.wa, x=x, stream=stream)
+        return x
+
+    def share_activations(self, other):
+        """Use another layer's x_perm, h and wa (of the same shape): for layers whose activations
+        are kept by save_act8 between their forward and their backward."""
+        if (self.dtype, self.x_perm.shape, self.h.shape) != (other.dtype, other.x_perm.shape,
+                                                             other.h.shape):
+            raise ValueError("layers of different shapes cannot share activation buffers")
+        self.x_perm, self.h, self.wa = other.x_perm, other.h, other.wa
+        self._graphs = {}  # captured steps hold the old buffers' pointers
+
     # ------------------------------------------------------------------ checkpoint / resume
     def checkpoint(self) -> dict:
         """The layer's whole training state as CPU tensors and host scalars: expert and router
@@ -160,7 +250,8 @@ class MoELayer:
                 "m": cpu(self.m), "v": cpu(self.v), "r_p": cpu(self.r_p), "r_m": cpu(self.r_m),
                 "r_v": cpu(self.r_v), "step_count": self.step_count, "lr": self.lr,
                 "betas": tuple(self.betas), "eps": self.eps, "renorm": self.renorm,
-                "dense_density": self.dense_density}
+                "dense_density": self.dense_density, "balance_coef": self.balance_coef,
+                "z_coef": self.z_coef}
 
     @classmethod
     def from_checkpoint(cls, ck: dict, device="cuda", group=None) -> "MoELayer":
@@ -169,7 +260,8 @@ class MoELayer:
         L = cls(T, H, E, k, I, ck["w_gate_up"].to(d), ck["w_down"].to(d), ck["w_router"].to(d),
                 ck["act"].to(d), lr=ck["lr"], betas=ck["betas"], eps=ck["eps"],
                 renorm=ck["renorm"], device=d, group=group,
-                dense_density=ck.get("dense_density", 0.015))
+                dense_density=ck.get("dense_density", 0.015),
+                balance_coef=ck.get("balance_coef", 0.0), z_coef=ck.get("z_coef", 0.0))
         L.set_active(ck["act"].to(d), ck["p"].to(d), ck["m"].to(d), ck["v"].to(d))
         L.r_p.copy_(ck["r_p"])
         L.r_m.copy_(ck["r_m"])
@@ -194,6 +286,8 @@ class MoELayer:
         self._check_tokens(x=x)
         B.route_topk(self.s, x, self.w_router, self.rt, logits_out=self.logits,
                      renorm=self.renorm, dev_status=self.status, ws=self.ws_route, stream=stream)
+        if self.aux:
+            self._aux_forward(stream, self.status)
 
     def _main(self, stream):
         return torch.cuda.current_stream(self.dev) if stream is None else stream
@@ -222,14 +316,17 @@ class MoELayer:
 
     def backward_into(self, x, dy, accumulate=0, dx=None, stream=None, dev_status=None):
         """The sparse backward with this set's masked-gradient plan; accumulate = 1 adds into
-        g_act and g_router (micro-batches)."""
+        g_act and g_router (micro-batches). With auxiliary losses on, their gradient joins
+        g_router and dx."""
+        status = self.status if dev_status is None else dev_status
         B.moe_bwd_sparse_planned(self.s, x, self.w_router, self.w_gate_up, self.w_down, self.rt,
                                  self.x_perm, self.h, self.wa, dy, self.act, self.g_act,
                                  self.g_router, plan=self.plan, n_dense=self.n_dense,
                                  accumulate=accumulate, dx=dx, logits=self.logits,
-                                 renorm=self.renorm,
-                                 dev_status=self.status if dev_status is None else dev_status,
-                                 ws=self.ws_bwd, stream=stream)
+                                 renorm=self.renorm, dev_status=status, ws=self.ws_bwd,
+                                 stream=stream)
+        if self.aux:
+            self._aux_backward(x, dx, stream, status)
 
     def optimizer_step(self, stream=None, skip_if_nonfinite=1):
         """Router update on the calling stream (the next routing reads it); expert update on the
@@ -324,6 +421,8 @@ class MoELayer:
             status.zero_()
             B.route_topk(self.s, x, self.w_router, self.rt, logits_out=self.logits,
                          renorm=self.renorm, dev_status=status, ws=self.ws_route, stream=cs)
+            if self.aux:
+                self._aux_forward(cs, status)
             fwd(B.FWD_GATHER)
         with torch.cuda.graph(g_up, stream=cs):
             fwd(B.FWD_GATE_UP)

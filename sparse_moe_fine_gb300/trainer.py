@@ -39,8 +39,16 @@ class StackTrainer:
     the input gradient dx of layer i+1 is the upstream gradient dy of layer i."""
 
     def __init__(self, layers, total_steps, lr_peak=2e-4, warmup_steps=0, reselect_every=50,
-                 reselect="rigl", drop_frac=0.3, skip_nonfinite=True, dense_exchange="allreduce"):
-        """dense_exchange (data parallel only): how the replicas agree on the importance phase's
+                 reselect="rigl", drop_frac=0.3, skip_nonfinite=True, dense_exchange="allreduce",
+                 act8=False):
+        """act8: keep each layer's activations in 8 bits between its forward and its backward
+        (usaf_act8_save / _restore). Layers of the same shape then share x_perm, h and wa, and all
+        layers two output and two input-gradient buffers per shape, so a layer below the top costs
+        17/16 bytes a value of x and h instead of its own bf16 buffers. The top layer's backward
+        follows its forward and reads its activations as they are. Layers' y and dx are then only
+        what the last call left there.
+
+        dense_exchange (data parallel only): how the replicas agree on the importance phase's
         gradient. "allreduce": every rank sums the whole dense gradient and selects alone;
         "reduce_scatter": every rank sums one part and the selection runs over the parts
         (dist_select), moving half the bytes and ranking 1/world of the entries per rank."""
@@ -58,6 +66,27 @@ class StackTrainer:
         self.step_no = 0
         self.history = []  # per step: lr, status words, turnover (device tensors until read)
         self._g_dense = [None] * len(self.layers)
+        self.act8 = bool(act8)
+        if self.act8:
+            self._share_buffers()
+
+    def _share_buffers(self):
+        """One x_perm, h, wa and restored input per layer shape, two y and two dx; a store per layer
+        below the top."""
+        first, self._x8, flow = {}, {}, {}
+        for i, L in enumerate(self.layers):
+            key = (L.dtype, tuple(L.x_perm.shape), tuple(L.h.shape), L.T)
+            if key not in first:
+                first[key] = L
+                self._x8[key] = torch.empty_like(L.y)
+            else:
+                L.share_activations(first[key])
+            tokens = (L.dtype, L.T, L.H)
+            ys, dxs = flow.setdefault((tokens, i % 2), (L.y, L.dx))
+            L.y, L.dx = ys, dxs
+            L._graphs = {}
+        self._key = [(L.dtype, tuple(L.x_perm.shape), tuple(L.h.shape), L.T) for L in self.layers]
+        self._stores = [B.ActStore8.empty(L.s, L.dev) for L in self.layers[:-1]]
 
     # ------------------------------------------------------------------ one micro-batch
     def _forward(self, x):
@@ -65,13 +94,18 @@ class StackTrainer:
         for L in self.layers:
             inputs.append(x)
             L.route(x)
-            x = L.forward(x)
+            y = L.forward(x)
+            if self.act8 and L is not self.layers[-1]:
+                L.save_act8(x, self._stores[len(inputs) - 1])
+            x = y
         return inputs
 
     def _backward(self, inputs, dy, first, dense):
         for i in reversed(range(len(self.layers))):
             L = self.layers[i]
             x = inputs[i]
+            if self.act8 and i < len(self.layers) - 1:
+                x = L.restore_act8(self._stores[i], self._x8[self._key[i]])
             dx = L.dx if i > 0 else None  # the bottom layer's input needs no gradient
             L.backward_into(x, dy, accumulate=0 if first else 1, dx=dx)
             if dense:
@@ -106,7 +140,8 @@ class StackTrainer:
             L.wait_optimizer()  # the expert update's status bits are in before they are kept
             status.append(L.status.clone())
         rec = {"step": n, "lr": lr, "status": status, "turnover": None,
-               "expert_count": [L.rt.expert_count.clone() for L in self.layers]}
+               "expert_count": [L.rt.expert_count.clone() for L in self.layers],
+               "aux_loss": [L.aux_loss.clone() if L.aux else None for L in self.layers]}
         if dense:
             rec["turnover"] = self._reselect()
         self.history.append(rec)
@@ -164,7 +199,8 @@ class StackTrainer:
     def metrics(self):
         """Host view of the recorded steps (synchronises): learning rate, whether the step was
         skipped for a non-finite gradient, turnover fraction at reselections, and the load
-        balance (largest expert count over the mean) per layer."""
+        balance (largest expert count over the mean) and, where they are on, the auxiliary losses
+        (total, balance, z) of the last micro-batch per layer."""
         torch.cuda.synchronize()
         out = []
         for r in self.history:
@@ -175,5 +211,6 @@ class StackTrainer:
             balance = [float(c.max().item()) / max(1e-9, float(c.float().mean().item()))
                        for c in r["expert_count"]]
             out.append({"step": r["step"], "lr": r["lr"], "skipped": skipped,
-                        "turnover": turnover, "load_balance": balance})
+                        "turnover": turnover, "load_balance": balance,
+                        "aux_loss": [None if a is None else a.tolist() for a in r["aux_loss"]]})
         return out
