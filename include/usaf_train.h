@@ -31,7 +31,7 @@ extern "C" {
  *   z       = 1/n sum_t logsumexp_e(logits[t,e])^2
  *   loss    = { coef_balance balance + coef_z z, balance, z };  all 0 when n = 0
  *   logits       [T,E] fp32, row t at logits + t * ld_logits (ld_logits >= E); -inf entries are
- *                experts the token cannot take; masked tokens are not read
+ *                experts the token cannot take; masked tokens' are ignored
  *   topk_idx     [T*k] expert of each slot, as usaf_route_topk writes it
  *   token_mask   [T] bytes, 0 = the token does not take part; NULL: every token does
  *   group_offset [G+1] first token of each group, non-decreasing; tokens before the first or from

@@ -214,7 +214,10 @@ class Routing:
                        torch.empty(cap, **i32), torch.empty(cap, **i32), torch.empty(R, **i32))
 
     def c(self) -> _Routing:
-        return _Routing(*[_ptr(getattr(self, f)) for f, _ in _Routing._fields_])
+        return _Routing(self.topk_idx.data_ptr(), self.topk_w.data_ptr(),
+                        self.expert_count.data_ptr(), self.expert_offset.data_ptr(),
+                        self.perm_tok.data_ptr(), self.perm_slot.data_ptr(),
+                        self.slot_row.data_ptr())
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:

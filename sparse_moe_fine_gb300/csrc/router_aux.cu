@@ -1,9 +1,11 @@
 // Load-balance loss, z-loss and per-expert counts of a router's logits, and their gradient
 // (usaf_router_aux_fwd / _bwd). Softmax statistics and sums are fp32, counts integers.
 //
-// A row of E logits is held by LPR neighbouring lanes, NV values each (expert sub + LPR i), so a
-// softmax is one read of the row, two butterflies and no shared memory; routers of at most 16
-// experts put several rows into a warp.
+// A row of E logits is held by LPR neighbouring lanes, NV values each, so a softmax is one read of
+// the row, two butterflies and no shared memory. Few lanes with many values beat the other way round:
+// a butterfly step costs the same for every lane of the warp, so four rows of eight lanes share what
+// one row of 32 would pay alone (and have two steps fewer). Only routers of more than 128 experts
+// use more lanes.
 #include <type_traits>
 
 #include "train.cuh"
@@ -16,9 +18,15 @@ constexpr int AUX_WARPS = 8;
 constexpr int AUX_THREADS = 32 * AUX_WARPS;
 constexpr int FIN_WARPS = 32;   // slot lanes of a final block, 32 experts wide
 constexpr int FIN_THREADS = 32 * FIN_WARPS;
-// Rows a warp has in flight: enough loads to cover DRAM's latency, 16 values a lane at most.
+// Rows that a lane has in flight: 16 values at most.
 template <int NV>
 constexpr int ROWS = NV <= 4 ? 4 : (NV <= 8 ? 2 : 1);
+// The expert of a lane's i-th value: four neighbours at a time, whether or not the rows' alignment
+// lets them be read as one vector, so that sums have one order and results do not depend on strides.
+template <int LPR, int NV>
+__device__ __forceinline__ int expert(int sub, int i) {
+  return NV >= 4 ? 4 * (sub + LPR * (i / 4)) + i % 4 : sub + LPR * i;
+}
 
 struct AuxParams {
   int64_t T, ld;
@@ -39,27 +47,47 @@ __device__ __forceinline__ int64_t clamp_off(const AuxParams& p, int g) {
   return o < 0 ? 0 : (o > p.T ? p.T : o);
 }
 
-// The group of token t (off[g] <= t < off[g + 1]), or -1.
-__device__ __forceinline__ int group_of(const AuxParams& p, int64_t t) {
-  if (!p.off) return 0;
-  int lo = 0, hi = p.G + 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (clamp_off(p, mid) <= t) lo = mid + 1;
-    else hi = mid;
+// The group offsets as a kernel looks them up: in shared memory where they fit (a binary search is
+// then a few cycles a step instead of a cache miss a step), else in place.
+constexpr int OFF_CAP = 1024;
+struct Groups {
+  const AuxParams& p;
+  const int32_t* s_off;
+  // fills s_off (all threads of the block, a barrier before its use) and checks its share
+  __device__ __forceinline__ Groups(const AuxParams& p_, int32_t* s) : p(p_), s_off(s) {
+    if (!p.off) return;
+    bool bad = false;
+    if (p.G < OFF_CAP) {
+      for (int i = threadIdx.x; i <= p.G; i += blockDim.x) {
+        const int o = p.off[i];
+        bad |= o < 0 || o > p.T || (i < p.G && p.off[i + 1] < o);
+        s[i] = o < 0 ? 0 : (o > p.T ? (int32_t)p.T : o);
+      }
+    } else {
+      for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i <= p.G;
+           i += (int64_t)gridDim.x * blockDim.x) {
+        const int o = p.off[i];
+        bad |= o < 0 || o > p.T || (i < p.G && p.off[i + 1] < o);
+      }
+    }
+    if (bad) flag_status(p.status, USAF_DEV_BAD_INDEX);
   }
-  return lo - 1 < p.G ? lo - 1 : -1;
-}
-
-__device__ __forceinline__ void check_offsets(const AuxParams& p, int64_t i0, int64_t stride) {
-  if (!p.off) return;
-  bool bad = false;
-  for (int64_t i = i0; i <= p.G; i += stride) {
-    const int o = p.off[i];
-    bad |= o < 0 || o > p.T || (i < p.G && p.off[i + 1] < o);
+  __device__ __forceinline__ int64_t at(int g) const {
+    if (!p.off) return g == 0 ? 0 : p.T;
+    return p.G < OFF_CAP ? s_off[g] : clamp_off(p, g);
   }
-  if (bad) flag_status(p.status, USAF_DEV_BAD_INDEX);
-}
+  // the group of token t (at(g) <= t < at(g + 1)), or -1
+  __device__ __forceinline__ int of(int64_t t) const {
+    if (!p.off) return 0;
+    int lo = 0, hi = p.G + 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (at(mid) <= t) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo - 1 < p.G ? lo - 1 : -1;
+  }
+};
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -106,15 +134,30 @@ __device__ __forceinline__ bool row_softmax(float (&v)[NV], float& lse) {
   return alive;
 }
 
-template <int LPR, int NV>
+// The row of token t, -inf where there is none; the mask is read beside it, not before it.
+// VEC: E and the row stride are multiples of four, the rows 16-byte aligned.
+template <int LPR, int NV, bool VEC>
 __device__ __forceinline__ void load_row(const AuxParams& p, int64_t t, bool in, int sub,
                                          float (&v)[NV]) {
   const float* row = p.logits + t * p.ld;
+  const bool keep = !(p.mask && in) || p.mask[t] != 0;
+  if constexpr (VEC) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = sub + LPR * i;
-    v[i] = in && e < p.E ? row[e] : -INFINITY;
+    for (int i = 0; i < NV; i += 4) {
+      const int e = expert<LPR, NV>(sub, i);
+      const float4 f = in && e < p.E ? *reinterpret_cast<const float4*>(row + e)
+                                     : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = expert<LPR, NV>(sub, i);
+      v[i] = in && e < p.E ? row[e] : -INFINITY;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = keep ? v[i] : -INFINITY;
 }
 
 __device__ __forceinline__ void write_loss(const AuxParams& p, double bal, double z, int64_t n,
@@ -132,7 +175,7 @@ __device__ __forceinline__ void write_loss(const AuxParams& p, double bal, doubl
 // One block per chunk of tokens. Per (chunk, group) that meet: the warps' rows are summed in
 // registers, then over rows of a warp and over the warps in a fixed order.
 // ONE: the only chunk; the block also forms the outputs and the loss (one launch).
-template <int LPR, int NV, bool ONE>
+template <int LPR, int NV, bool VEC, bool ONE>
 __global__ void __launch_bounds__(AUX_THREADS)
     aux_part_kernel(const AuxParams p, AuxWs w, int32_t* __restrict__ count_out,
                     float* __restrict__ prob_out, int32_t* __restrict__ n_out,
@@ -148,8 +191,9 @@ __global__ void __launch_bounds__(AUX_THREADS)
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane % LPR, rw = lane / LPR;
   const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
-  check_offsets(p, (int64_t)blockIdx.x * blockDim.x + threadIdx.x,
-                (int64_t)gridDim.x * blockDim.x);
+  dep_launch();
+  __shared__ int32_t s_off[OFF_CAP];
+  const Groups groups(p, s_off);
   for (int e = threadIdx.x; e < p.E; e += AUX_THREADS) s_cnt[e] = 0;
   if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *w.arrived = 0;  // for the final kernel
   if constexpr (ONE) {
@@ -162,15 +206,16 @@ __global__ void __launch_bounds__(AUX_THREADS)
   double bal_all = 0.0, z_all = 0.0;  // ONE: of this thread's experts / of thread 0
   int64_t n_all = 0;
   bool badidx = false;
+  __syncthreads();
   int64_t t = t0;
   while (t < t1) {
-    const int g = group_of(p, t);
+    const int g = groups.of(t);
     if (g < 0) {  // before the first group or behind the last
-      const int64_t f = clamp_off(p, 0);
+      const int64_t f = groups.at(0);
       t = f > t ? f : t1;
       continue;
     }
-    int64_t te = min(t1, clamp_off(p, g + 1));
+    int64_t te = min(t1, groups.at(g + 1));
     if (te <= t) te = t + 1;  // only where the offsets decrease
     __syncthreads();  // the last segment's counts are out; ONE: the zeroed outputs too
     // the segment's first expert indices, on their way while the rows are read
@@ -189,7 +234,7 @@ __global__ void __launch_bounds__(AUX_THREADS)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t tok = base + u * AUX_WARPS * RPW + rw;
-        load_row<LPR, NV>(p, tok, tok < te && (!p.mask || p.mask[tok] != 0), sub, v[u]);
+        load_row<LPR, NV, VEC>(p, tok, tok < te, sub, v[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -215,7 +260,7 @@ __global__ void __launch_bounds__(AUX_THREADS)
     if (rw == 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = sub + LPR * i;
+        const int e = expert<LPR, NV>(sub, i);
         if (e < p.E) s_prob[wid * p.E + e] = acc[i];
       }
     }
@@ -293,6 +338,8 @@ __global__ void __launch_bounds__(FIN_THREADS)
   float a = 0.f, z = 0.f;
   int32_t c = 0, n = 0;
   const int64_t o0 = clamp_off(p, g), o1 = clamp_off(p, g + 1);
+  dep_launch();
+  dep_wait();
   if (o1 > o0) {
     const int64_t ch1 = (o1 - 1) / p.chunk;
 #pragma unroll 8
@@ -346,8 +393,8 @@ __global__ void __launch_bounds__(FIN_THREADS)
   if (!s_last) return;
   __threadfence();
   // fixed order: thread t its share of the blocks and groups, then a tree
-  __shared__ double r_b[FIN_THREADS], r_z[FIN_THREADS];
-  __shared__ int64_t r_n[FIN_THREADS];
+  __shared__ double r_b[FIN_WARPS], r_z[FIN_WARPS];
+  __shared__ int64_t r_n[FIN_WARPS];
   double sb = 0.0, sz = 0.0;
   int64_t sn = 0;
   for (int64_t i = threadIdx.x; i < gridDim.x; i += FIN_THREADS) sb += __ldcg(w.bal + i);
@@ -355,23 +402,30 @@ __global__ void __launch_bounds__(FIN_THREADS)
     sz += __ldcg(w.group_z + i);
     sn += __ldcg(n_tok + i);
   }
-  r_b[threadIdx.x] = sb;
-  r_z[threadIdx.x] = sz;
-  r_n[threadIdx.x] = sn;
-  __syncthreads();
-  for (int h = FIN_THREADS / 2; h; h >>= 1) {
-    if (threadIdx.x < h) {
-      r_b[threadIdx.x] += r_b[threadIdx.x + h];
-      r_z[threadIdx.x] += r_z[threadIdx.x + h];
-      r_n[threadIdx.x] += r_n[threadIdx.x + h];
+  auto tree = [&] {
+    for (int o = 16; o; o >>= 1) {
+      sb += __shfl_xor_sync(0xffffffffu, sb, o);
+      sz += __shfl_xor_sync(0xffffffffu, sz, o);
+      sn += __shfl_xor_sync(0xffffffffu, sn, o);
     }
-    __syncthreads();
+  };
+  tree();
+  if (lane == 0) {
+    r_b[wid] = sb;
+    r_z[wid] = sz;
+    r_n[wid] = sn;
   }
-  if (threadIdx.x == 0) write_loss(p, r_b[0], r_z[0], r_n[0], loss);
+  __syncthreads();
+  if (wid != 0) return;
+  sb = r_b[lane];
+  sz = r_z[lane];
+  sn = r_n[lane];
+  tree();
+  if (lane == 0) write_loss(p, sb, sz, sn, loss);
 }
 
 // The gradient: each row is read once, its group's counts stay in registers while the group lasts.
-template <int LPR, int NV>
+template <int LPR, int NV, bool VEC>
 __global__ void __launch_bounds__(AUX_THREADS)
     aux_bwd_kernel(const AuxParams p, const int32_t* __restrict__ count,
                    const int32_t* __restrict__ n_tok, const float* __restrict__ d_loss, float* out,
@@ -380,8 +434,20 @@ __global__ void __launch_bounds__(AUX_THREADS)
   constexpr int RPW = 32 / LPR, U = ROWS<NV>;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane % LPR, rw = lane / LPR;
-  check_offsets(p, (int64_t)blockIdx.x * blockDim.x + threadIdx.x,
-                (int64_t)gridDim.x * blockDim.x);
+  __shared__ int32_t s_off[OFF_CAP];
+  dep_wait();
+  dep_launch();
+  const int64_t first = ((int64_t)blockIdx.x * AUX_WARPS + wid) * RPW * rows_per_lane;
+  float v[U][NV];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t tok = first + (r0 + u) * RPW + rw;
+      load_row<LPR, NV, VEC>(p, tok, r0 + u < rows_per_lane && tok < p.T, sub, v[u]);
+    }
+  };
+  load(0);  // on their way while the counts are looked up
+  const Groups groups(p, s_off);
   int64_t n = 0;
   for (int i = threadIdx.x; i < p.G; i += AUX_THREADS) n += n_tok[i];
   for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -393,7 +459,6 @@ __global__ void __launch_bounds__(AUX_THREADS)
   const float up = d_loss ? *d_loss : 1.f;
   const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
   const float zc = p.coef_z != 0.f ? up * 2.f * p.coef_z * inv_n : 0.f;
-  const int64_t first = ((int64_t)blockIdx.x * AUX_WARPS + wid) * RPW * rows_per_lane;
   int cur = -2;       // group whose counts are in c
   int64_t cur_end = 0;
   float c[NV], cg = 0.f;
@@ -402,27 +467,20 @@ __global__ void __launch_bounds__(AUX_THREADS)
   bool bad = false;
   for (int r0 = 0; r0 < rows_per_lane; r0 += U) {
     if (first + r0 * RPW >= p.T) break;
-    float v[U][NV];
-    bool in_group[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t tok = first + (r0 + u) * RPW + rw;
-      in_group[u] = r0 + u < rows_per_lane && tok < p.T && (!p.mask || p.mask[tok] != 0);
-      load_row<LPR, NV>(p, tok, in_group[u], sub, v[u]);
-    }
+    if (r0 > 0) load(r0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t tok = first + (r0 + u) * RPW + rw;
       const bool in = r0 + u < rows_per_lane && tok < p.T;
       if (in && (cur == -2 || tok >= cur_end)) {
-        cur = group_of(p, tok);
-        cur_end = cur >= 0 ? clamp_off(p, cur + 1) : (tok < clamp_off(p, 0) ? clamp_off(p, 0) : p.T);
+        cur = groups.of(tok);
+        cur_end = cur >= 0 ? groups.at(cur + 1) : (tok < groups.at(0) ? groups.at(0) : p.T);
         const int ng = cur >= 0 ? n_tok[cur] : 0;
         cg = p.coef_b != 0.f && ng > 0 ? up * p.coef_b * p.share * inv_n / (float)ng : 0.f;
         if (cur >= 0) {
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
-            const int e = sub + LPR * i;
+            const int e = expert<LPR, NV>(sub, i);
             c[i] = e < p.E ? (float)count[(int64_t)cur * p.E + e] : 0.f;
           }
         }
@@ -440,10 +498,27 @@ __global__ void __launch_bounds__(AUX_THREADS)
       if (in) {
         float* o = out + tok * ld_out;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int e = sub + LPR * i;
-          if (e < p.E) {
-            float d = v[u][i] * fmaf(cg, c[i] - s, zt);
+        for (int i = 0; i < NV; ++i) v[u][i] *= fmaf(cg, c[i] - s, zt);
+        if constexpr (VEC) {
+#pragma unroll
+          for (int i = 0; i < NV; i += 4) {
+            const int e = expert<LPR, NV>(sub, i);
+            if (e >= p.E) continue;
+            float4* at = reinterpret_cast<float4*>(o + e);
+            float4 d = make_float4(v[u][i], v[u][i + 1], v[u][i + 2], v[u][i + 3]);
+            if (accumulate) {
+              const float4 old = *at;
+              d.x += old.x, d.y += old.y, d.z += old.z, d.w += old.w;
+            }
+            *at = d;
+            bad |= !finite_f(d.x) || !finite_f(d.y) || !finite_f(d.z) || !finite_f(d.w);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int e = expert<LPR, NV>(sub, i);
+            if (e >= p.E) continue;
+            float d = v[u][i];
             if (accumulate) d += o[e];
             o[e] = d;
             bad |= !finite_f(d);
@@ -475,30 +550,42 @@ AuxParams make_params(const AuxArgs& a) {
   return p;
 }
 
-// Calls f with the lanes per row and values per lane of E experts.
+// Calls f with the lanes per row and values per lane of E experts, and whether 16-byte vectors serve
+// (`vec`: the rows allow them).
 template <class F>
-usaf_status by_width(int E, F f) {
-  using std::integral_constant;
-#define USAF_W(L, N) f(integral_constant<int, L>(), integral_constant<int, N>())
-  if (E <= 8) return USAF_W(8, 1);
-  if (E <= 16) return USAF_W(16, 1);
-  if (E <= 32) return USAF_W(32, 1);
-  if (E <= 64) return USAF_W(32, 2);
-  if (E <= 128) return USAF_W(32, 4);
-  if (E <= 256) return USAF_W(32, 8);
-  if (E <= 512) return USAF_W(32, 16);
-  return USAF_W(32, 32);
+usaf_status by_width(int E, bool vec, F f) {
+#define USAF_W(L, N)                                                                              \
+  do {                                                                                            \
+    if constexpr (N >= 4)                                                                         \
+      if (vec)                                                                                    \
+        return f(std::integral_constant<int, L>(), std::integral_constant<int, N>(),              \
+                 std::true_type());                                                               \
+    return f(std::integral_constant<int, L>(), std::integral_constant<int, N>(),                  \
+             std::false_type());                                                                  \
+  } while (0)
+  if (E <= 8) USAF_W(8, 1);
+  if (E <= 16) USAF_W(8, 2);
+  if (E <= 32) USAF_W(8, 4);
+  if (E <= 64) USAF_W(8, 8);
+  if (E <= 128) USAF_W(8, 16);
+  if (E <= 256) USAF_W(16, 16);
+  if (E <= 512) USAF_W(32, 16);
+  USAF_W(32, 32);
 #undef USAF_W
+}
+
+bool rows_vec(const float* base, int64_t ld, int E) {
+  return E % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(base) & 15) == 0;
 }
 
 }  // namespace
 
-// Tokens of a chunk. A batch of at most eight rows a warp is one chunk, whose block forms the outputs
-// itself (one launch); longer ones have about two chunks per SM.
+// Tokens of a chunk. A batch of at most four rounds of the block's warps is one chunk, whose block forms the
+// outputs itself (one launch); longer ones have up to four chunks per SM.
 int64_t aux_chunk_tokens(int64_t T, int64_t E) {
-  const int64_t rows = E <= 8 ? 4 : (E <= 16 ? 2 : 1);  // of a warp at a time
-  if (T <= 8 * AUX_WARPS * rows) return T;
-  const int64_t c = round_up(ceil_div(T, 2 * 152), 32);
+  const int64_t rows = E <= 128 ? 4 : (E <= 256 ? 2 : 1);  // of a warp at a time
+  if (T <= 4 * AUX_WARPS * rows) return T;
+  const int64_t c = round_up(ceil_div(T, 4 * 152), 32);
   return c < 32 ? 32 : c;
 }
 
@@ -518,7 +605,7 @@ usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, in
   const AuxParams p = make_params(a);
   const size_t smem = (size_t)(AUX_WARPS + 1) * a.E * 4 + p.chunk;
   const bool one = p.nchunks == 1;
-  USAF_TRY(by_width(a.E, [&](auto lpr, auto nv) {
+  USAF_TRY(by_width(a.E, rows_vec(a.logits, a.ld, a.E), [&](auto lpr, auto nv, auto vec) {
     USAF_TRACE("router_aux_part", st);
     auto go = [&](auto kernel) {
       if (smem > 48 * 1024 &&
@@ -529,16 +616,14 @@ usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, in
       USAF_CHECK_LAUNCH();
       return USAF_OK;
     };
-    return one ? go(aux_part_kernel<lpr.value, nv.value, true>)
-               : go(aux_part_kernel<lpr.value, nv.value, false>);
+    return one ? go(aux_part_kernel<lpr.value, nv.value, vec.value, true>)
+               : go(aux_part_kernel<lpr.value, nv.value, vec.value, false>);
   }));
   if (one) return USAF_OK;
   USAF_TRACE("router_aux_final", st);
   const int nb = (int)ceil_div(a.E, 32);  // blocks of a group
-  aux_final_kernel<<<(unsigned)(nb * a.G), FIN_THREADS, 0, st>>>(p, w, nb, count, prob_sum, n_tok,
-                                                                 loss);
-  USAF_CHECK_LAUNCH();
-  return USAF_OK;
+  return launch_dep(aux_final_kernel, dim3((unsigned)(nb * a.G)), FIN_THREADS, 0, st, p, w, nb,
+                    count, prob_sum, n_tok, loss);
 }
 
 usaf_status aux_bwd_launch(const AuxArgs& a, const int32_t* count, const int32_t* n_tok,
@@ -546,17 +631,16 @@ usaf_status aux_bwd_launch(const AuxArgs& a, const int32_t* count, const int32_t
                            cudaStream_t st) {
   const AuxParams p = make_params(a);
   USAF_TRACE("router_aux_bwd", st);
-  return by_width(a.E, [&](auto lpr, auto nv) {
+  const bool rows_ok = rows_vec(a.logits, a.ld, a.E) && rows_vec(dlogit, ld_out, a.E);
+  return by_width(a.E, rows_ok, [&](auto lpr, auto nv, auto vec) {
     constexpr int RPW = 32 / lpr.value;
     // rows per lane group: enough blocks for every SM first, then rows that share a count load
     const int64_t lanes = (int64_t)AUX_WARPS * RPW;
     int rows = 1;
-    while (rows < 16 && ceil_div(a.T, lanes * rows * 2) >= 2 * 152) rows *= 2;
+    while (rows < 8 && ceil_div(a.T, lanes * rows * 2) >= 4 * 152) rows *= 2;
     const unsigned grid = (unsigned)ceil_div(a.T, lanes * rows);
-    aux_bwd_kernel<lpr.value, nv.value><<<grid, AUX_THREADS, 0, st>>>(
-        p, count, n_tok, d_loss, dlogit, ld_out, accumulate, rows);
-    USAF_CHECK_LAUNCH();
-    return USAF_OK;
+    return launch_dep(aux_bwd_kernel<lpr.value, nv.value, vec.value>, dim3(grid), AUX_THREADS, 0, st, p, count,
+                      n_tok, d_loss, dlogit, ld_out, accumulate, rows);
   });
 }
 

@@ -6,6 +6,33 @@
 
 namespace usaf {
 
+// A kernel that may be set up while the one before it in the stream still runs: it must pass
+// dep_wait() before it touches memory that other kernels write or read. A kernel lets the next one
+// in by dep_launch(); one that never does lets it in when it ends.
+__device__ __forceinline__ void dep_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void dep_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... P, class... A>
+usaf_status launch_dep(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                       cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? USAF_OK
+                                                                                  : USAF_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------- router auxiliary losses
 struct AuxArgs {
   int64_t T, G, ld;
