@@ -1,5 +1,6 @@
 // The two products of a dense router gradient (usaf_router_grad): g_router = g_in + dlogit^T x and
-// dx = dx_in + dlogit w_router.
+// dx = dx_in + dlogit w_router. Here for fp32 tokens, on CUDA cores in fp32; bf16 tokens are in
+// router_grad_tc.cu.
 #include "train.cuh"
 
 namespace usaf {
@@ -11,12 +12,11 @@ constexpr int DX_T = 64, DX_H = 64, DX_E = 32;  // tile of dx, experts per step
 
 // part[s][e][h] = sum over the tokens of split s of dlogit[t,e] x[t,h]; with one split the result
 // goes to g_router (+ g_in).
-template <typename T>
 __global__ void __launch_bounds__(256)
     router_grad_w_kernel(const RouterGradArgs a, int64_t per_split, float* __restrict__ part) {
   __shared__ float s_d[RG_T][RG_E];
   __shared__ float s_x[RG_T][RG_H];
-  const T* x = static_cast<const T*>(a.x);
+  const float* x = static_cast<const float*>(a.x);
   const int h0 = blockIdx.x * RG_H, e0 = blockIdx.y * RG_E;
   const int64_t t0 = blockIdx.z * per_split, t1 = min(a.T, t0 + per_split);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;  // 4 h, 2 e
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(256)
     }
     for (int i = threadIdx.x; i < RG_T * RG_H; i += 256) {
       const int r = i / RG_H, c = i % RG_H;
-      s_x[r][c] = t + r < t1 && h0 + c < a.H ? to_f32(x[(t + r) * a.H + h0 + c]) : 0.f;
+      s_x[r][c] = t + r < t1 && h0 + c < a.H ? x[(t + r) * a.H + h0 + c] : 0.f;
     }
     __syncthreads();
 #pragma unroll 8
@@ -79,12 +79,11 @@ __global__ void __launch_bounds__(256)
   flag_status_warp(a.status, bad, USAF_DEV_NONFINITE);
 }
 
-template <typename T>
 __global__ void __launch_bounds__(256) router_grad_x_kernel(const RouterGradArgs a) {
   __shared__ float s_d[DX_T][DX_E + 1];
   __shared__ float s_w[DX_E][DX_H];
-  const T* dx_in = static_cast<const T*>(a.dx_in);
-  T* dx = static_cast<T*>(a.dx);
+  const float* dx_in = static_cast<const float*>(a.dx_in);
+  float* dx = static_cast<float*>(a.dx);
   const int h0 = blockIdx.x * DX_H;
   const int64_t t0 = (int64_t)blockIdx.y * DX_T;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
@@ -121,8 +120,8 @@ __global__ void __launch_bounds__(256) router_grad_x_kernel(const RouterGradArgs
       const int64_t t = t0 + ty * 4 + u;
       const int h = h0 + tx * 4 + q;
       if (t >= a.T || h >= a.H) continue;
-      const float v = (dx_in ? to_f32(dx_in[t * a.H + h]) : 0.f) + acc[u][q];
-      dx[t * a.H + h] = from_f32<T>(v);
+      const float v = (dx_in ? dx_in[t * a.H + h] : 0.f) + acc[u][q];
+      dx[t * a.H + h] = v;
       bad |= !finite_f(v);
     }
   flag_status_warp(a.status, bad, USAF_DEV_NONFINITE);
@@ -153,13 +152,12 @@ usaf_status launch_w(const RouterGradArgs& a, float* part, cudaStream_t st) {
                   (unsigned)ceil_div(a.T, per));
   {
     USAF_TRACE("router_grad_w", st);
-    router_grad_w_kernel<float><<<grid, 256, 0, st>>>(a, per, part);
+    router_grad_w_kernel<<<grid, 256, 0, st>>>(a, per, part);
     USAF_CHECK_LAUNCH();
   }
   return grid.z > 1 ? launch_reduce(a, part, grid.z, st) : USAF_OK;
 }
 
-template <typename T>
 usaf_status launch_x(const RouterGradArgs& a, cudaStream_t st) {
   USAF_TRACE("router_grad_x", st);
   const int64_t rows = ceil_div(a.T, DX_T);
@@ -169,11 +167,11 @@ usaf_status launch_x(const RouterGradArgs& a, cudaStream_t st) {
     const int64_t skip = r0 * DX_T;
     b.T = a.T - skip;
     b.dlogit = a.dlogit + skip * a.ld;
-    b.dx_in = a.dx_in ? static_cast<const T*>(a.dx_in) + skip * a.H : nullptr;
-    b.dx = static_cast<T*>(a.dx) + skip * a.H;
+    b.dx_in = a.dx_in ? static_cast<const float*>(a.dx_in) + skip * a.H : nullptr;
+    b.dx = static_cast<float*>(a.dx) + skip * a.H;
     const int64_t n = rows - r0 < 65535 ? rows - r0 : 65535;
     if (b.T > n * DX_T) b.T = n * DX_T;
-    router_grad_x_kernel<T><<<dim3((unsigned)ceil_div(a.H, DX_H), (unsigned)n), 256, 0, st>>>(b);
+    router_grad_x_kernel<<<dim3((unsigned)ceil_div(a.H, DX_H), (unsigned)n), 256, 0, st>>>(b);
     USAF_CHECK_LAUNCH();
   }
   return USAF_OK;
@@ -183,24 +181,18 @@ usaf_status launch_x(const RouterGradArgs& a, cudaStream_t st) {
 
 void router_grad_ws_layout(int64_t T, int64_t E, int64_t H, usaf_dtype dt, Carver& c,
                            RouterGradWs& w) {
-  const int64_t s = dt == USAF_BF16 ? ceil_div(T, router_grad_tc_split(T, E, H))
-                                    : splits_for(T, E, H);
+  if (dt == USAF_BF16) {
+    router_grad_tc_layout(T, E, H, c, w);
+    return;
+  }
+  const int64_t s = splits_for(T, E, H);
   w.g_part = c.take<float>(s > 1 ? s * E * H : 1);
 }
 
 usaf_status router_grad_launch(const RouterGradArgs& a, const RouterGradWs& w, cudaStream_t st) {
-  if (a.dt == USAF_F32) {
-    if (a.g_router) USAF_TRY(launch_w(a, w.g_part, st));
-    return a.dx ? launch_x<float>(a, st) : USAF_OK;
-  }
-  if (a.g_router) {
-    const int64_t per = router_grad_tc_split(a.T, a.E, a.H);
-    USAF_TRY(router_grad_w_tc(a, w.g_part, per, st));
-    if (per < a.T) USAF_TRY(launch_reduce(a, w.g_part, ceil_div(a.T, per), st));
-  }
-  if (!a.dx) return USAF_OK;
-  // the tensor-core kernel keeps the router's columns of at most 256 experts in shared memory
-  return router_grad_x_tc_ok(a.E) ? router_grad_x_tc(a, st) : launch_x<__nv_bfloat16>(a, st);
+  if (a.dt == USAF_BF16) return router_grad_tc(a, w, st);
+  if (a.g_router) USAF_TRY(launch_w(a, w.g_part, st));
+  return a.dx ? launch_x(a, st) : USAF_OK;
 }
 
 }  // namespace usaf

@@ -7,9 +7,8 @@
 // the same with what is left gives three bf16 numbers whose sum is exactly the float (8 bits each of
 // its 24), and a product of two bf16 numbers is exact in fp32. g_router, an fp32 result, uses all
 // three parts of dlogit (x is bf16 already). dx is rounded to bf16 at the end, so two parts of
-// dlogit and of w (2^-16 each) and three of their four products are enough. The converting warps
-// read dlogit as fp32 and write the parts into shared memory in the layout the MMA reads, so no
-// split copy ever goes through memory.
+// dlogit and of w (2^-16 each) and three of their four products are enough. A first kernel writes
+// the parts (6 bytes a logit, which stay in L2); the products' kernels are then fed by TMA alone.
 #include "tc_ptx.cuh"
 #include "train.cuh"
 
@@ -19,22 +18,12 @@ using namespace tcx;
 
 namespace {
 
-constexpr int CONV_WARPS = 8;  // converting warps of either kernel; g_router's then run the epilogue
+// Part q of the E experts' logits starts at column q * part_cols(E) of a row of three parts.
+__host__ __device__ constexpr int part_cols(int E) { return (E + 7) / 8 * 8; }
+// Expert rows of w's parts: whole steps of the contraction, zero past E.
+__host__ __device__ constexpr int w_rows(int E) { return (E + 15) / 16 * 16; }
 
-// Eight neighbouring logits' gradients, zero past the experts' end or for a row that is not there.
-__device__ __forceinline__ void load8(const float* row, bool in, int e, int E, bool vec,
-                                      float (&v)[8]) {
-  if (in && vec && e + 8 <= E) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(row + e));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(row + e + 4));
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = in && e + i < E ? __ldg(row + e + i) : 0.f;
-  }
-}
-// The next truncated part of eight values; they become what it leaves.
+// ------------------------------------------------------------------------------ parts
 __device__ __forceinline__ uint4 take_part(float (&v)[8]) {
   uint4 p;
   p.x = trunc_bf16x2(v[0], v[1]);
@@ -45,213 +34,250 @@ __device__ __forceinline__ uint4 take_part(float (&v)[8]) {
   for (int i = 0; i < 8; ++i) v[i] = trunc_rest(v[i]);
   return p;
 }
-__device__ __forceinline__ uint4 round_part(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
+
+// One thread per eight logits of a token, then one per eight columns of w (when w is given).
+__global__ void __launch_bounds__(256)
+    router_grad_split_kernel(const float* __restrict__ dl, int64_t ld, int64_t T, int E, int vec,
+                             __nv_bfloat16* __restrict__ parts, const float* __restrict__ w, int H,
+                             __nv_bfloat16* __restrict__ wparts) {
+  dep_launch();
+  const int ec = part_cols(E) / 8, hc = H / 8;
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  float v[8];
+  if (i < T * ec) {
+    const int64_t t = i / ec;
+    const int e = (int)(i - t * ec) * 8;
+    const float* row = dl + t * ld + e;
+    if (vec && e + 8 <= E) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(row));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(row) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = e + j < E ? __ldg(row + j) : 0.f;
+    }
+    uint4* to = reinterpret_cast<uint4*>(parts + t * 3 * part_cols(E) + e);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) to[q * ec] = take_part(v);
+    return;
+  }
+  i -= T * ec;
+  if (!w || i >= (int64_t)w_rows(E) * hc) return;
+  const int e = (int)(i / hc);
+  const int64_t c = i - (int64_t)e * hc;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  if (e < E) {
+    const float4* from = reinterpret_cast<const float4*>(w + (int64_t)e * H) + 2 * c;
+    const float4 a = __ldg(from), b = __ldg(from + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  uint4* to = reinterpret_cast<uint4*>(wparts);
+  to[i] = take_part(v);
+  to[(int64_t)w_rows(E) * hc + i] =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                 pack_bf16x2(v[6], v[7]));
 }
 
 // ------------------------------------------------------------------------------ g_router
-// A CTA owns 128 expert rows (M) by 256 features (N) over one part of the tokens (K).
-// A = dlogit's parts, 64 tokens x 128 experts each, experts contiguous (MN-major); B = x boxes of 64
-// features x 64 tokens by TMA (MN-major). Routers of at most 40 experts put the three parts side by
-// side into one 128-row A (STACK): one MMA instead of three, the rows added in the epilogue.
-// Otherwise the leading parts' products and the smaller ones have accumulators of their own.
+// A CTA owns 128 expert rows (M) by 256 features (N) over one stretch of the tokens (K). A = dlogit's
+// parts, 32 tokens x 128 experts, experts contiguous (MN-major); B = x, 32 tokens x 256 features
+// (MN-major). Routers of at most 40 experts have their three parts side by side in one 128-row A
+// (STACK): one MMA instead of three, the rows added at the end. Otherwise the leading part and the
+// two smaller ones have accumulators of their own.
+// The tensor core adds to its accumulator with truncation, an error that grows with the number of
+// additions (1.8e-8 a step here), so the leading accumulator is emptied every FLUSH blocks (16
+// steps) into fp32 registers of the epilogue warps, which round to nearest. The smaller parts' sums
+// are 2^-8 of it and need no such care; their MMAs run while it is read. (STACK: two accumulators
+// take turns.) Error in norm against 64 bits at 16,383 tokens: 1.0e-6 without, 3e-7 with.
 namespace gw {
-constexpr int BK = 64;
+constexpr int BK = 32;
 constexpr int N = 256;
-constexpr int PART_BYTES = 128 * BK * 2;
-constexpr int BOX_BYTES = 64 * BK * 2;
-constexpr int B_BYTES = 4 * BOX_BYTES;
-constexpr int NA = 2;
+constexpr int BOX = 64 * BK * 2;
+constexpr int B_BYTES = 4 * BOX;
+constexpr int FLUSH = 8;
+constexpr int EPI_WARPS = 8;
 constexpr int OUT_PITCH = N + 4;  // floats per row of the tile in the epilogue
-constexpr int THREADS = 64 + 32 * CONV_WARPS;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
 template <bool STACK>
 struct Cfg {
   static constexpr int PARTS = STACK ? 1 : 3;
-  static constexpr int NB = STACK ? 5 : 3;
-  static constexpr int A_BYTES = PARTS * PART_BYTES;
-  static constexpr int RING = NA * A_BYTES + NB * B_BYTES;
+  static constexpr int NS = STACK ? 8 : 5;
+  static constexpr int A_BYTES = PARTS * 2 * BOX;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int RING = NS * STAGE;
   static constexpr int SMEM = RING + 1024 + 256;
-  static_assert(128 * OUT_PITCH * 4 <= RING, "output tile in the rings");
+  static_assert(128 * OUT_PITCH * 4 <= RING, "output tile in the ring");
   static_assert(SMEM <= 232448, "shared memory");
 };
 struct Params {
-  int64_t T, ld;
+  int64_t T;
   int E, H;
   int64_t per_split;
-  const float* dl;
   const float* g_in;
-  float* out;      // g_router, or the parts' sums [splits][E][H]
-  int whole;       // one split: out is g_router
-  int vec;         // dlogit's rows allow 16-byte loads
+  float* out;      // g_router, or the stretches' sums [splits][E][H]
+  int whole;       // one stretch: out is g_router
   uint32_t* status;
 };
 }  // namespace gw
 
 template <bool STACK>
 __global__ void __launch_bounds__(gw::THREADS, 1)
-    router_grad_w_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const gw::Params p) {
+    router_grad_w_tc_kernel(const __grid_constant__ CUtensorMap tm_d,
+                            const __grid_constant__ CUtensorMap tm_x, const gw::Params p) {
   using C = gw::Cfg<STACK>;
   using namespace gw;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + NA * C::A_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING);
-  // fullA[NA], emptyA[NA], fullB[NB], emptyB[NB], done
-  const uint32_t fullA = smem_u32(bars), emptyA = fullA + 8 * NA, fullB = emptyA + 8 * NA,
-                 emptyB = fullB + 8 * C::NB, done = emptyB + 8 * C::NB;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NA + 2 * C::NB + 1);
+  // full[NS], empty[NS], taken[2] (accumulator complete), given[2] (accumulator read), done
+  const uint32_t full = smem_u32(bars), empty = full + 8 * C::NS, taken = empty + 8 * C::NS,
+                 given = taken + 16, done = given + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::NS + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  constexpr uint32_t COLS = STACK ? N : 2 * N;
+  constexpr uint32_t COLS = 2 * N;  // STACK: two accumulators; else leading part | smaller parts
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int h0 = blockIdx.x * N, e0 = blockIdx.y * 128;
   const int64_t t0 = blockIdx.z * p.per_split;
   const int64_t t1 = min(p.T, t0 + p.per_split);
   const int nkb = (int)((t1 - t0 + BK - 1) / BK);
   const int nbox = min(4, (p.H - h0) / 64);
-  const int ep = (min(p.E - e0, 128) + 7) / 8 * 8;  // experts of the tile, in whole chunks of 8
+  const int ep = STACK ? part_cols(p.E) : min(part_cols(p.E) - e0, 128);
+  const int na = (STACK ? 3 * ep : ep) > 64 ? 2 : 1;  // 64-expert boxes of a part
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NA; ++i) {
-      mbar_init(fullA + 8 * i, CONV_WARPS);
-      mbar_init(emptyA + 8 * i, 1);
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < C::NB; ++i) {
-      mbar_init(fullB + 8 * i, 1);
-      mbar_init(emptyB + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(taken + 8 * i, 1);
+      mbar_init(given + 8 * i, EPI_WARPS);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), COLS);
-  // expert rows that no conversion writes (past the router's end, past the stacked parts) are zero
-  if (STACK || ep < 128)
-    for (int i = threadIdx.x; i < NA * C::A_BYTES / 16; i += THREADS)
-      reinterpret_cast<uint4*>(sA)[i] = make_uint4(0, 0, 0, 0);
-  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  dep_wait();    // the parts are written
+  dep_launch();  // dx's kernel may start: it reads the parts, and waits before it reads the sums
 
   if (warp == 0) {
-    if (lane == 0) {  // ------------------------------------------------ x boxes
+    if (lane == 0) {  // ------------------------------------------------ loads
       int issued = 0;
       bool ok = true;
       for (int kb = 0; kb < nkb; ++kb) {
-        const int s = kb % C::NB;
-        ok = mbar_wait(emptyB + 8 * s, ((kb / C::NB) & 1) ^ 1, abort_flag);
+        const int s = kb % C::NS;
+        ok = mbar_wait(empty + 8 * s, ((kb / C::NS) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        mbar_expect_tx(fullB + 8 * s, nbox * BOX_BYTES);
-        for (int b = 0; b < nbox; ++b)
-          tma_load_2d(smem_u32(sB + s * B_BYTES + b * BOX_BYTES), &tm_x, fullB + 8 * s,
-                      h0 + 64 * b, (int)(t0 + (int64_t)kb * BK));
+        const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + C::A_BYTES, fb = full + 8 * s;
+        const int t = (int)(t0 + (int64_t)kb * BK);
+        mbar_expect_tx(fb, (C::PARTS * na + nbox) * BOX);
+        for (int q = 0; q < C::PARTS; ++q)
+          for (int i = 0; i < na; ++i)
+            tma_load_2d(a + (2 * q + i) * BOX, &tm_d, fb, q * part_cols(p.E) + e0 + 64 * i, t);
+        for (int i = 0; i < nbox; ++i) tma_load_2d(b + i * BOX, &tm_x, fb, h0 + 64 * i, t);
         ++issued;
       }
       if (!ok) *abort_flag = 1;
       const long long deadline = clock64() + TIMEOUT_CYCLES;  // every copy lands before the end
-      for (int s = 0; s < C::NB && s < issued; ++s) {
-        const int last = issued - 1 - ((issued - 1 - s) % C::NB);
-        mbar_drain(fullB + 8 * s, (last / C::NB) & 1, deadline);
+      for (int s = 0; s < C::NS && s < issued; ++s) {
+        const int last = issued - 1 - ((issued - 1 - s) % C::NS);
+        mbar_drain(full + 8 * s, (last / C::NS) & 1, deadline);
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {  // ------------------------------------------------ MMAs
       const uint32_t idesc = idesc_bf16(64 * nbox, true, true);
-      const uint64_t ad0 = sdesc(smem_u32(sA), 8192, 1024);
-      const uint64_t bd0 = sdesc(smem_u32(sB), BOX_BYTES, 1024);
+      const uint64_t ad0 = sdesc(smem_u32(smem), BOX, 1024);
+      const uint64_t bd0 = sdesc(smem_u32(smem) + C::A_BYTES, BOX, 1024);
       bool ok = true;
       for (int kb = 0; kb < nkb; ++kb) {
-        const int sa = kb % NA, sb = kb % C::NB;
-        ok = mbar_wait(fullA + 8 * sa, (kb / NA) & 1, abort_flag) &&
-             mbar_wait(fullB + 8 * sb, (kb / C::NB) & 1, abort_flag);
+        const int s = kb % C::NS;
+        ok = mbar_wait(full + 8 * s, (kb / C::NS) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t a = ad0 + ((sa * C::A_BYTES) >> 4), b = bd0 + ((sb * B_BYTES) >> 4);
-#pragma unroll
-        for (int part = 0; part < C::PARTS; ++part)
+        const uint64_t a = ad0 + ((s * C::STAGE) >> 4), b = bd0 + ((s * C::STAGE) >> 4);
+        auto part = [&](uint32_t d, int q, bool fresh) {
 #pragma unroll
           for (int ks = 0; ks < BK / 16; ++ks)
-            umma_bf16(tmem + (part ? N : 0), a + ((part * PART_BYTES + ks * 2048) >> 4),
-                      b + ((ks * 2048) >> 4), idesc,
-                      kb > 0 || ks > 0 || part == 2 ? 1u : 0u);
-        umma_commit(emptyA + 8 * sa);
-        umma_commit(emptyB + 8 * sb);
+            umma_bf16(d, a + ((q * 2 * BOX + ks * 2048) >> 4), b + ((ks * 2048) >> 4), idesc,
+                      fresh && ks == 0 ? 0u : 1u);
+        };
+        if constexpr (!STACK) {
+          part(tmem + N, 1, kb == 0);
+          part(tmem + N, 2, false);
+        }
+        const int turn = kb / FLUSH, acc = STACK ? turn & 1 : 0;
+        const bool fresh = kb % FLUSH == 0;
+        if (fresh) {  // the accumulator's last sums have been read
+          const int use = STACK ? turn >> 1 : turn;  // how often it has been used before
+          ok = mbar_wait(given + 8 * acc, (use & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        part(tmem + acc * N, 0, fresh);
+        umma_commit(empty + 8 * s);
+        if (kb % FLUSH == FLUSH - 1 || kb == nkb - 1) umma_commit(taken + 8 * acc);
       }
       if (!ok) *abort_flag = 1;
       umma_commit(done);
       mbar_drain(done, 0, clock64() + TIMEOUT_CYCLES);
     }
-  } else {  // ---------------------------------------------------- parts of dlogit
-    const int ct = threadIdx.x - 64;
-    const int chunks = ep / 8;                  // chunks of eight experts per token
-    const int per = (BK * chunks + 255) / 256;  // chunks per thread, at most 4
-    float v[4][8];
-    auto load = [&](int kb) {
+  } else {  // ---------------------------------------------------- epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
+    const int rows = STACK ? 3 * ep : ep;
+    float sum[4][32];  // this lane's row, 128 columns
+    const int nch = q * 32 < rows ? min(4, (nbox * 64 - half * 128) / 32) : 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = ct + 256 * u;
-        if (u >= per || i >= BK * chunks) continue;
-        const int tk = i / chunks, c = i - tk * chunks;
-        const int64_t t = t0 + (int64_t)kb * BK + tk;
-        load8(p.dl + t * p.ld, t < t1, e0 + 8 * c, p.E, p.vec != 0, v[u]);
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
+    auto add = [&](uint32_t from) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= nch) break;
+#pragma unroll
+        for (int i = 0; i < 32; i += 16) {
+          float d[16];
+          tmem_ld16(from + c * 32 + i, d);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[c][i + j] += d[j];
+        }
       }
     };
     bool ok = true;
-    if (nkb > 0) load(0);
-    for (int kb = 0; kb < nkb; ++kb) {
-      const int sa = kb % NA;
-      ok = mbar_wait_warp(emptyA + 8 * sa, ((kb / NA) & 1) ^ 1, abort_flag);
+    for (int turn = 0; turn * FLUSH < nkb; ++turn) {
+      const int acc = STACK ? turn & 1 : 0, use = STACK ? turn >> 1 : turn;
+      ok = mbar_wait_warp(taken + 8 * acc, use & 1, abort_flag);
       if (!ok) break;
-      uint8_t* a = sA + sa * C::A_BYTES;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = ct + 256 * u;
-        if (u >= per || i >= BK * chunks) continue;
-        const int tk = i / chunks, c = i - tk * chunks;
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          // chunk of the 128 rows; 64 rows to a box, the chunk's place swizzled by the token
-          const int m = STACK ? c + part * chunks : c;
-          uint8_t* dst = a + (STACK ? 0 : part * PART_BYTES) + (m >> 3) * 8192 + tk * 128 +
-                         (((m & 7) ^ (tk & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) = take_part(v[u]);
-        }
-      }
-      fence_async_smem();
+      tc_fence_after();
+      add(ta + acc * N);
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(fullA + 8 * sa);
-      if (kb + 1 < nkb) load(kb + 1);
+      if (lane == 0) mbar_arrive(given + 8 * acc);
     }
-    // ---------------------------------------------------------------- epilogue
-    // tensor memory -> the rings (free after the last MMA) -> whole rows of global memory
-    float* tile = reinterpret_cast<float*>(smem);
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const int row = q * 32 + lane;
     if (ok) ok = mbar_wait_warp(done, 0, abort_flag);
     if (ok && *abort_flag == 0) {
       tc_fence_after();
-      const int rows = STACK ? 3 * ep : ep;
-      for (int ch = half * 4; ch < half * 4 + 4; ++ch) {
-        if (ch * 32 >= nbox * 64) break;
-        if (q * 32 < rows) {
-          float d[32];
-          const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + ch * 32;
-          tmem_ld32(ta, d);
-          if constexpr (!STACK) {
-            float lo[32];
-            tmem_ld32(ta + N, lo);
+      if constexpr (!STACK) add(ta + N);
+      // registers -> the ring (free after the last MMA), for whole rows of global memory
+      float* tile = reinterpret_cast<float*>(smem) + (q * 32 + lane) * OUT_PITCH + half * 128;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) d[j] += lo[j];
-          }
-          float4* dst = reinterpret_cast<float4*>(tile + row * OUT_PITCH + ch * 32);
+      for (int c = 0; c < 4; ++c) {
+        if (c >= nch) break;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            dst[j] = make_float4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
-        }
+        for (int j = 0; j < 8; ++j)
+          reinterpret_cast<float4*>(tile + c * 32)[j] = make_float4(
+              sum[c][4 * j], sum[c][4 * j + 1], sum[c][4 * j + 2], sum[c][4 * j + 3]);
       }
     }
   }
@@ -297,46 +323,88 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
   }
 }
 
+// g_router = g_in + the stretches' sums in their order: thread i of n
+__device__ __forceinline__ void reduce_parts(const float* part, int splits, int64_t count,
+                                             const float* g_in, float* g, uint32_t* status,
+                                             int64_t i0, int64_t n) {
+  bool bad = false;
+  for (int64_t i = i0 * 4; i < count; i += n * 4) {  // count = E H is a multiple of 64
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+      float4 d[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (s0 + u < splits) d[u] = __ldcg(reinterpret_cast<const float4*>(part + (s0 + u) * count + i));
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (s0 + u < splits) v.x += d[u].x, v.y += d[u].y, v.z += d[u].z, v.w += d[u].w;
+    }
+    float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // g_in and g_router need no alignment
+      if (g_in) r[j] += g_in[i + j];
+      bad |= !finite_f(r[j]);
+      g[i + j] = r[j];
+    }
+  }
+  flag_status_warp(status, bad, USAF_DEV_NONFINITE);
+}
+__global__ void __launch_bounds__(256)
+    router_grad_sum_kernel(const float* part, int splits, int64_t count, const float* g_in,
+                           float* g, uint32_t* status) {
+  dep_wait();
+  reduce_parts(part, splits, count, g_in, g, status, (int64_t)blockIdx.x * 256 + threadIdx.x,
+               (int64_t)gridDim.x * 256);
+}
+
 // ------------------------------------------------------------------------------ dx
-// A CTA keeps the router's columns [h0, h0 + 128) in shared memory, two bf16 parts, and walks token
-// tiles of 128: A = dlogit's two parts (K-major, 64 experts a block) through a ring, accumulators in
-// tensor memory, twice. dx_in comes and dx goes by TMA through a ring of 128 x 64 boxes in which the
-// epilogue adds: the token rows are read and written in whole lines while the next tile converts.
+// A CTA owns 128 features and walks token tiles of 128: A = dlogit's two leading parts (K-major, 64
+// experts a block) through a ring, B = w's two parts, accumulators in tensor memory, twice. RES: B
+// for all experts stays in shared memory (at most 256 experts); else it comes through the ring with
+// A. dx_in comes and dx goes by TMA through a ring of 128 x 64 boxes in which the epilogue adds, so
+// token rows are read and written in whole lines while later tiles are on their way.
+// The same launch adds up g_router's stretches at its end (`sum`), which saves one of its own.
 namespace gx {
 constexpr int TM = 128;      // tokens of a tile
 constexpr int NH = 128;      // features of a CTA
 constexpr int KB = 64;       // experts of an A block
 constexpr int A_PART = TM * KB * 2;
 constexpr int A_BYTES = 2 * A_PART;
-constexpr int NA = 2;
+constexpr int B_BLOCK = 2 * 2 * KB * 128;  // w's two parts, two groups of 64 features, KB experts
 constexpr int BOX = TM * 64 * 2;
-constexpr int MAX_E = 256;
+constexpr int NA = 2;
+constexpr int MAX_RES = 256;
 constexpr int MAX_SLOTS = 6;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * (EPI_WARPS + CONV_WARPS);
+constexpr int THREADS = 96 + 32 * EPI_WARPS;
 constexpr int SMEM_MAX = 232448;
-// bytes of the router's two parts for ke experts (a multiple of 16): two groups of 64 features
-__host__ __device__ constexpr int b_bytes(int ke) { return 2 * 2 * ke * 128; }
+__host__ __device__ constexpr int b_bytes(int ke) {  // of the resident parts, or of NA blocks
+  return ke <= MAX_RES ? 2 * 2 * ke * 128 : NA * B_BLOCK;
+}
 __host__ __device__ constexpr int slots(int ke) {
   const int s = (SMEM_MAX - 1024 - 512 - NA * A_BYTES - b_bytes(ke)) / BOX;
   return s < MAX_SLOTS ? s : MAX_SLOTS;
 }
-static_assert(slots(MAX_E) >= 2, "staging for one tile");
+static_assert(slots(MAX_RES) >= 2 && slots(1024) >= 2, "staging for one tile");
 struct Params {
-  int64_t T, ld;
+  int64_t T;
   int E, H, ke;
   int slots;
   int per_group;   // CTAs that share a feature group
-  const float* dl;
-  const float* w;
   int add;         // dx_in is there
-  int vec;
   uint32_t* status;
+  const float* sum;  // g_router's stretches to add up, or null
+  int splits;
+  const float* g_in;
+  float* g_router;
 };
 }  // namespace gx
 
+template <bool RES>
 __global__ void __launch_bounds__(gx::THREADS, 1)
-    router_grad_x_tc_kernel(const __grid_constant__ CUtensorMap tm_in,
+    router_grad_x_tc_kernel(const __grid_constant__ CUtensorMap tm_d,
+                            const __grid_constant__ CUtensorMap tm_w,
+                            const __grid_constant__ CUtensorMap tm_in,
                             const __grid_constant__ CUtensorMap tm_out, const gx::Params p) {
   using namespace gx;
   extern __shared__ uint8_t smem_raw[];
@@ -345,13 +413,13 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   const int ke = p.ke, NS = p.slots;
   uint8_t* sA = smem;
   uint8_t* sStage = smem + NA * A_BYTES;
-  uint8_t* sB = sStage + NS * BOX;  // [part][feature group of 64][expert][64 features]
+  uint8_t* sB = sStage + NS * BOX;  // [part][feature group of 64][expert][64 features] (a block)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sB + b_bytes(ke));
-  // fullA[NA], emptyA[NA], tfull[2], tempty[2], loaded[NS], added[NS], freed[NS], done
-  const uint32_t fullA = smem_u32(bars), emptyA = fullA + 8 * NA, tfull = emptyA + 8 * NA,
+  // full[NA], empty[NA], tfull[2], tempty[2], loaded[NS], added[NS], freed[NS], done, wfull
+  const uint32_t full = smem_u32(bars), empty = full + 8 * NA, tfull = empty + 8 * NA,
                  tempty = tfull + 16, loaded = tempty + 16, added = loaded + 8 * MAX_SLOTS,
-                 freed = added + 8 * MAX_SLOTS, done = freed + 8 * MAX_SLOTS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NA + 4 + 3 * MAX_SLOTS + 1);
+                 freed = added + 8 * MAX_SLOTS, done = freed + 8 * MAX_SLOTS, wfull = done + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NA + 4 + 3 * MAX_SLOTS + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr uint32_t COLS = 2 * NH;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -361,12 +429,13 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   const int tiles = (int)((p.T + TM - 1) / TM);
   const int nbox = min(2, (p.H - h0) / 64);
   const int nkb = (ke + KB - 1) / KB;
-  const int part_b = 2 * ke * 128;
+  const int brows = RES ? ke : KB;                       // expert rows of a feature group of B
+  const int part_b = 2 * brows * 128;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NA; ++i) {
-      mbar_init(fullA + 8 * i, CONV_WARPS);
-      mbar_init(emptyA + 8 * i, 1);
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull + 8 * i, 1);
@@ -378,41 +447,95 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
       mbar_init(freed + 8 * i, 1);
     }
     mbar_init(done, 1);
+    mbar_init(wfull, 1);
     *abort_flag = 0;
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(tmem_slot), COLS);
-  // the router's columns: expert row of 128 bytes (64 features), 16-byte chunks swizzled by the row
-  for (int i = threadIdx.x; i < ke * 16; i += THREADS) {
-    const int e = i >> 4, c = i & 15;
-    float v[8];
-    const int h = h0 + 8 * c;
-    if (e < p.E && h < p.H) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p.w + (int64_t)e * p.H + h));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(p.w + (int64_t)e * p.H + h + 4));
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    }
-    uint8_t* dst = sB + (c >> 3) * ke * 128 + e * 128 + (((c & 7) ^ (e & 7)) << 4);
-    *reinterpret_cast<uint4*>(dst) = take_part(v);
-    *reinterpret_cast<uint4*>(dst + part_b) = round_part(v);
-  }
-  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!p.sum) dep_wait();  // else the kernel before is g_router's, which saw the parts written
   bool bad = false;
 
   if (warp == 0) {
+    if (lane == 0) {  // ------------------------------------------------ A and B blocks
+      const long long limit = TIMEOUT_CYCLES;
+      bool ok = true;
+      int kc = 0;
+      if constexpr (RES) {
+        mbar_expect_tx(wfull, 2 * nbox * ke * 128);
+        for (int q = 0; q < 2; ++q)
+          for (int i = 0; i < nbox; ++i)
+            tma_load_2d(smem_u32(sB + q * part_b + i * ke * 128), &tm_w, wfull, h0 + 64 * i,
+                        q * ke);
+      }
+      for (int t = first; t < tiles && ok; t += p.per_group)
+        for (int kb = 0; kb < nkb; ++kb, ++kc) {
+          const int s = kc % NA;
+          ok = mbar_wait(empty + 8 * s, ((kc / NA) & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          const uint32_t a = smem_u32(sA + s * A_BYTES), fb = full + 8 * s;
+          mbar_expect_tx(fb, A_BYTES + (RES ? 0 : nbox * 2 * KB * 128));
+          for (int q = 0; q < 2; ++q)
+            tma_load_2d(a + q * A_PART, &tm_d, fb, q * part_cols(p.E) + kb * KB, t * TM);
+          if constexpr (!RES) {
+            for (int q = 0; q < 2; ++q)
+              for (int i = 0; i < nbox; ++i)
+                tma_load_2d(smem_u32(sB + s * B_BLOCK + q * part_b + i * KB * 128), &tm_w, fb,
+                            h0 + 64 * i, q * ke + kb * KB);
+          }
+        }
+      if (!ok) *abort_flag = 1;
+      const long long deadline = clock64() + limit;
+      if constexpr (RES) mbar_drain(wfull, 0, deadline);
+      for (int s = 0; s < NA && s < kc; ++s) {
+        const int last = kc - 1 - ((kc - 1 - s) % NA);
+        mbar_drain(full + 8 * s, (last / NA) & 1, deadline);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {  // ------------------------------------------------ MMAs
+      const uint32_t idesc = idesc_bf16(64 * nbox, false, true);
+      const uint64_t ad0 = sdesc(smem_u32(sA), 16, 1024);
+      const uint64_t bd0 = sdesc(smem_u32(sB), brows * 128, 1024);
+      int n = 0, kc = 0;
+      bool ok = true;
+      if constexpr (RES) ok = mbar_wait(wfull, 0, abort_flag);
+      for (int t = first; t < tiles && ok; t += p.per_group, ++n) {
+        ok = mbar_wait(tempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, abort_flag);
+        if (!ok) break;
+        const uint32_t d = tmem + (n & 1) * NH;
+        for (int kb = 0; kb < nkb; ++kb, ++kc) {
+          const int s = kc % NA;
+          ok = mbar_wait(full + 8 * s, (kc / NA) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = ad0 + ((s * A_BYTES) >> 4);
+          const uint64_t b = bd0 + ((RES ? kb * KB * 128 : s * B_BLOCK) >> 4);
+          const int steps = min(KB / 16, ke / 16 - kb * (KB / 16));
+          for (int ks = 0; ks < steps; ++ks) {
+            const uint64_t ah = a + ((ks * 32) >> 4), am = ah + (A_PART >> 4);
+            const uint64_t bh = b + ((ks * 2048) >> 4), bm = bh + (part_b >> 4);
+            umma_bf16(d, ah, bh, idesc, kb > 0 || ks > 0 ? 1u : 0u);
+            umma_bf16(d, ah, bm, idesc, 1u);
+            umma_bf16(d, am, bh, idesc, 1u);
+          }
+          umma_commit(empty + 8 * s);
+        }
+        if (ok) umma_commit(tfull + 8 * (n & 1));
+      }
+      if (!ok) *abort_flag = 1;
+      umma_commit(done);
+      mbar_drain(done, 0, clock64() + TIMEOUT_CYCLES);
+    }
+  } else if (warp == 2) {
     if (lane == 0) {  // ------------------------------------------------ dx_in boxes
       int u = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += p.per_group)
-        for (int b = 0; b < nbox && ok; ++b, ++u) {
+        for (int b = 0; b < nbox && ok; ++b) {
           const int s = u % NS;
           ok = mbar_wait(freed + 8 * s, ((u / NS) & 1) ^ 1, abort_flag);
           if (!ok) break;
@@ -422,51 +545,18 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
           } else {
             mbar_arrive(loaded + 8 * s);
           }
+          ++u;
         }
       if (!ok) *abort_flag = 1;
-      const int issued = u;  // boxes 0 .. u - 1
       const long long deadline = clock64() + TIMEOUT_CYCLES;
-      for (int s = 0; s < NS && s < issued; ++s) {
-        const int last = issued - 1 - ((issued - 1 - s) % NS);
+      for (int s = 0; s < NS && s < u; ++s) {
+        const int last = u - 1 - ((u - 1 - s) % NS);
         mbar_drain(loaded + 8 * s, (last / NS) & 1, deadline);
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {  // ------------------------------------------------ MMAs
-      const uint32_t idesc = idesc_bf16(64 * nbox, false, true);
-      const uint64_t ad0 = sdesc(smem_u32(sA), 16, 1024);
-      const uint64_t bd0 = sdesc(smem_u32(sB), ke * 128, 1024);
-      int n = 0, kc = 0;
-      bool ok = true;
-      for (int t = first; t < tiles && ok; t += p.per_group, ++n) {
-        ok = mbar_wait(tempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, abort_flag);
-        if (!ok) break;
-        const uint32_t d = tmem + (n & 1) * NH;
-        for (int kb = 0; kb < nkb; ++kb, ++kc) {
-          const int sa = kc % NA;
-          ok = mbar_wait(fullA + 8 * sa, (kc / NA) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a = ad0 + ((sa * A_BYTES) >> 4);
-          const int steps = min(KB / 16, ke / 16 - kb * (KB / 16));
-          for (int ks = 0; ks < steps; ++ks) {
-            const uint64_t ah = a + ((ks * 32) >> 4), am = ah + (A_PART >> 4);
-            const uint64_t bh = bd0 + (((kb * 4 + ks) * 2048) >> 4), bm = bh + (part_b >> 4);
-            umma_bf16(d, ah, bh, idesc, kb > 0 || ks > 0 ? 1u : 0u);
-            umma_bf16(d, ah, bm, idesc, 1u);
-            umma_bf16(d, am, bh, idesc, 1u);
-          }
-          umma_commit(emptyA + 8 * sa);
-        }
-        if (ok) umma_commit(tfull + 8 * (n & 1));
-      }
-      if (!ok) *abort_flag = 1;
-      umma_commit(done);
-      mbar_drain(done, 0, clock64() + TIMEOUT_CYCLES);
-    }
-  } else if (warp < 2 + EPI_WARPS) {  // ------------------------- epilogue: add and store
-    const int q = warp & 3, b = (warp - 2) >> 2;  // lanes' quarter, box of the tile
-    const bool issuer = ((warp - 2) & 3) == 0 && lane == 0;
+  } else {  // ---------------------------------------------------- epilogue: add and store
+    const int q = warp & 3, b = (warp - 3) >> 2;  // lanes' quarter, box of the tile
+    const bool issuer = ((warp - 3) & 3) == 0 && lane == 0;
     const int row = q * 32 + lane;
     if (b < nbox) {
       int n = 0;
@@ -524,41 +614,6 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
       if (issuer) bulk_wait();
       __syncwarp();
     }
-  } else {  // ---------------------------------------------------- dlogit's parts
-    const int ct = threadIdx.x - 64 - 32 * EPI_WARPS;
-    // 128 tokens x 8 chunks of eight experts: four a thread
-    float v[4][8];
-    auto load = [&](int t, int kb) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = ct + 256 * u, tk = i >> 3, c = i & 7;
-        const int64_t tok = (int64_t)t * TM + tk;
-        const int e = kb * KB + 8 * c;
-        if (e < ke) load8(p.dl + tok * p.ld, tok < p.T, e, p.E, p.vec != 0, v[u]);
-      }
-    };
-    int kc = 0;
-    bool ok = true;
-    if (first < tiles) load(first, 0);
-    for (int t = first; t < tiles && ok; t += p.per_group)
-      for (int kb = 0; kb < nkb; ++kb, ++kc) {
-        const int sa = kc % NA;
-        ok = mbar_wait_warp(emptyA + 8 * sa, ((kc / NA) & 1) ^ 1, abort_flag);
-        if (!ok) break;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = ct + 256 * u, tk = i >> 3, c = i & 7;
-          if (kb * KB + 8 * c >= ke) continue;
-          uint8_t* dst = sA + sa * A_BYTES + tk * 128 + ((c ^ (tk & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) = take_part(v[u]);
-          *reinterpret_cast<uint4*>(dst + A_PART) = round_part(v[u]);
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(fullA + 8 * sa);
-        if (kb + 1 < nkb) load(t, kb + 1);
-        else if (t + p.per_group < tiles) load(t + p.per_group, 0);
-      }
   }
   flag_status_warp(p.status, bad, USAF_DEV_NONFINITE);
   tc_fence_before();
@@ -568,88 +623,119 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
     tc_fence_after();
     tmem_free(tmem, COLS);
   }
+  if (p.sum) {
+    dep_wait();  // every stretch's sums are there
+    reduce_parts(p.sum, p.splits, (int64_t)p.E * p.H, p.g_in, p.g_router, p.status,
+                 (int64_t)blockIdx.x * THREADS + threadIdx.x, (int64_t)gridDim.x * THREADS);
+  }
 }
 
-bool rows_vec(const RouterGradArgs& a) {
-  return a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.dlogit) & 15) == 0;
+template <class K>
+bool grow_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+         cudaSuccess;
 }
 
 template <bool STACK>
-usaf_status launch_w(const CUtensorMap& tm, const gw::Params& p, dim3 grid, cudaStream_t st) {
+usaf_status launch_w(const CUtensorMap& d, const CUtensorMap& x, const gw::Params& p, dim3 grid,
+                     cudaStream_t st) {
   USAF_TRACE("router_grad_w", st);
   using C = gw::Cfg<STACK>;
-  if (cudaFuncSetAttribute(router_grad_w_tc_kernel<STACK>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return USAF_ERR_CUDA;
-  router_grad_w_tc_kernel<STACK><<<grid, gw::THREADS, C::SMEM, st>>>(tm, p);
-  USAF_CHECK_LAUNCH();
-  return USAF_OK;
+  if (!grow_smem(router_grad_w_tc_kernel<STACK>, C::SMEM)) return USAF_ERR_CUDA;
+  return launch_dep(router_grad_w_tc_kernel<STACK>, grid, gw::THREADS, C::SMEM, st, d, x, p);
+}
+
+template <bool RES>
+usaf_status launch_x(const CUtensorMap& d, const CUtensorMap& w, const CUtensorMap& in,
+                     const CUtensorMap& out, const gx::Params& p, unsigned grid, cudaStream_t st) {
+  USAF_TRACE("router_grad_x", st);
+  if (!grow_smem(router_grad_x_tc_kernel<RES>, gx::SMEM_MAX)) return USAF_ERR_CUDA;
+  const int smem = gx::NA * gx::A_BYTES + p.slots * gx::BOX + gx::b_bytes(p.ke) + 1024 + 512;
+  return launch_dep(router_grad_x_tc_kernel<RES>, dim3(grid), gx::THREADS, smem, st, d, w, in, out,
+                    p);
+}
+
+// Tokens of a stretch of g_router's sum: about one CTA per SM, whole blocks, at least 128 tokens.
+int64_t stretch(int64_t T, int64_t E, int64_t H) {
+  const int64_t tiles = ceil_div(H, gw::N) * ceil_div(E, 128);
+  const int64_t s = tiles < 152 ? 152 / tiles : 1;
+  const int64_t per = round_up(ceil_div(T, s), gw::BK);
+  return per < 128 ? 128 : per;
 }
 
 }  // namespace
 
-// Tokens of a split of g_router's sum: about one CTA per SM, whole blocks of 64 tokens, at least two.
-int64_t router_grad_tc_split(int64_t T, int64_t E, int64_t H) {
-  const int64_t tiles = ceil_div(H, gw::N) * ceil_div(E, 128);
-  const int64_t s = tiles < 152 ? 152 / tiles : 1;
-  const int64_t per = round_up(ceil_div(T, s), gw::BK);
-  return per < 2 * gw::BK ? 2 * gw::BK : per;
+void router_grad_tc_layout(int64_t T, int64_t E, int64_t H, Carver& c, RouterGradWs& w) {
+  w.parts = c.take<uint16_t>(T * 3 * part_cols((int)E));
+  w.w_parts = c.take<uint16_t>(2 * w_rows((int)E) * H);
+  const int64_t s = ceil_div(T, stretch(T, E, H));
+  w.g_part = c.take<float>(s > 1 ? s * E * H : 1);
 }
 
-usaf_status router_grad_w_tc(const RouterGradArgs& a, float* part, int64_t per_split,
-                             cudaStream_t st) {
-  CUtensorMap tm;
-  if (!map_bf16_2d(&tm, a.x, a.H, a.T, 64, gw::BK)) return USAF_ERR_CUDA;
-  const int64_t splits = ceil_div(a.T, per_split);
-  gw::Params p{};
-  p.T = a.T;
-  p.ld = a.ld;
-  p.E = (int)a.E;
-  p.H = (int)a.H;
-  p.per_split = per_split;
-  p.dl = a.dlogit;
-  p.g_in = a.g_in;
-  p.whole = splits == 1;
-  p.out = p.whole ? a.g_router : part;
-  p.vec = rows_vec(a);
-  p.status = a.status;
-  const dim3 grid((unsigned)ceil_div(a.H, gw::N), (unsigned)ceil_div(a.E, 128), (unsigned)splits);
-  // three parts of round_up(E, 8) rows fit the 128 of one A
-  return round_up(a.E, 8) <= 40 ? launch_w<true>(tm, p, grid, st) : launch_w<false>(tm, p, grid, st);
-}
-
-bool router_grad_x_tc_ok(int64_t E) { return E <= gx::MAX_E; }
-
-usaf_status router_grad_x_tc(const RouterGradArgs& a, cudaStream_t st) {
-  USAF_TRACE("router_grad_x", st);
-  CUtensorMap in, out;
-  if (!map_bf16_2d(&out, a.dx, a.H, a.T, 64, gx::TM) ||
-      !map_bf16_2d(&in, a.dx_in ? a.dx_in : a.dx, a.H, a.T, 64, gx::TM))
+usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cudaStream_t st) {
+  const int E = (int)a.E, H = (int)a.H, ep = part_cols(E), ke = w_rows(E);
+  __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(ws.parts);
+  __nv_bfloat16* wparts = static_cast<__nv_bfloat16*>(ws.w_parts);
+  {
+    USAF_TRACE("router_grad_split", st);
+    const int64_t n = a.T * (ep / 8) + (a.dx ? (int64_t)ke * (H / 8) : 0);
+    const int vec = a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.dlogit) & 15) == 0;
+    router_grad_split_kernel<<<(unsigned)ceil_div(n, 256), 256, 0, st>>>(
+        a.dlogit, a.ld, a.T, E, vec, parts, a.dx ? a.w_router : nullptr, H, wparts);
+    USAF_CHECK_LAUNCH();
+  }
+  const int64_t per = stretch(a.T, E, H), splits = ceil_div(a.T, per);
+  if (a.g_router) {
+    CUtensorMap d, x;
+    if (!map_bf16_2d(&d, parts, 3 * ep, a.T, 64, gw::BK) ||
+        !map_bf16_2d(&x, a.x, H, a.T, 64, gw::BK))
+      return USAF_ERR_CUDA;
+    gw::Params p{};
+    p.T = a.T;
+    p.E = E;
+    p.H = H;
+    p.per_split = per;
+    p.g_in = a.g_in;
+    p.whole = splits == 1;
+    p.out = p.whole ? a.g_router : ws.g_part;
+    p.status = a.status;
+    const dim3 grid((unsigned)ceil_div(H, gw::N), (unsigned)ceil_div(E, 128), (unsigned)splits);
+    // three parts fit the 128 rows of one A
+    USAF_TRY(ep <= 40 ? launch_w<true>(d, x, p, grid, st) : launch_w<false>(d, x, p, grid, st));
+  }
+  const bool sum = a.g_router && splits > 1;
+  if (!a.dx) {
+    if (!sum) return USAF_OK;
+    USAF_TRACE("router_grad_sum", st);
+    return launch_dep(router_grad_sum_kernel, dim3(grid_dim_for(a.E * a.H / 4)), 256, 0, st,
+                      ws.g_part, (int)splits, a.E * a.H, a.g_in, a.g_router, a.status);
+  }
+  CUtensorMap d, w, in, out;
+  const uint32_t wrows = ke <= gx::MAX_RES ? ke : gx::KB;
+  if (!map_bf16_2d(&d, parts, 3 * ep, a.T, 64, gx::TM) ||
+      !map_bf16_2d(&w, wparts, H, 2 * ke, 64, wrows) ||
+      !map_bf16_2d(&out, a.dx, H, a.T, 64, gx::TM) ||
+      !map_bf16_2d(&in, a.dx_in ? a.dx_in : a.dx, H, a.T, 64, gx::TM))
     return USAF_ERR_CUDA;
   gx::Params p{};
   p.T = a.T;
-  p.ld = a.ld;
-  p.E = (int)a.E;
-  p.H = (int)a.H;
-  p.ke = (int)round_up(a.E, 16);
-  p.slots = gx::slots(p.ke);
-  p.dl = a.dlogit;
-  p.w = a.w_router;
+  p.E = E;
+  p.H = H;
+  p.ke = ke;
+  p.slots = gx::slots(ke);
   p.add = a.dx_in != nullptr;
-  p.vec = rows_vec(a);
   p.status = a.status;
-  const int64_t groups = ceil_div(a.H, gx::NH), tiles = ceil_div(a.T, gx::TM);
-  int64_t per = device_sm_count() / groups;
-  if (per < 1) per = 1;
-  if (per > tiles) per = tiles;
-  p.per_group = (int)per;
-  const int smem = gx::NA * gx::A_BYTES + p.slots * gx::BOX + gx::b_bytes(p.ke) + 1024 + 512;
-  if (cudaFuncSetAttribute(router_grad_x_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           gx::SMEM_MAX) != cudaSuccess)
-    return USAF_ERR_CUDA;
-  router_grad_x_tc_kernel<<<(unsigned)(groups * per), gx::THREADS, smem, st>>>(in, out, p);
-  USAF_CHECK_LAUNCH();
-  return USAF_OK;
+  p.sum = sum ? ws.g_part : nullptr;
+  p.splits = (int)splits;
+  p.g_in = a.g_in;
+  p.g_router = a.g_router;
+  const int64_t groups = ceil_div(H, gx::NH), tiles = ceil_div(a.T, gx::TM);
+  int64_t most = device_sm_count() / groups;
+  if (most < 1) most = 1;
+  p.per_group = (int)(most < tiles ? most : tiles);
+  const unsigned grid = (unsigned)(groups * p.per_group);
+  return ke <= gx::MAX_RES ? launch_x<true>(d, w, in, out, p, grid, st)
+                           : launch_x<false>(d, w, in, out, p, grid, st);
 }
 
 }  // namespace usaf

@@ -77,17 +77,16 @@ struct RouterGradArgs {
   uint32_t* status;
 };
 struct RouterGradWs {
-  float* g_part;  // [splits][E][H] sums of g_router over parts of the tokens
+  float* g_part;  // [splits][E][H] sums of g_router over stretches of the tokens
+  void* parts;    // bf16 layers: [T][3][experts in eights] dlogit in three bf16 parts
+  void* w_parts;  // [2][experts in sixteens][H] w_router in two bf16 parts
 };
 void router_grad_ws_layout(int64_t T, int64_t E, int64_t H, usaf_dtype dt, Carver& c,
                            RouterGradWs& w);
 usaf_status router_grad_launch(const RouterGradArgs& a, const RouterGradWs& w, cudaStream_t st);
-// tensor-core products (bf16 x, dx): tokens of a split of g_router's sum, the two kernels
-int64_t router_grad_tc_split(int64_t T, int64_t E, int64_t H);
-usaf_status router_grad_w_tc(const RouterGradArgs& a, float* part, int64_t per_split,
-                             cudaStream_t st);
-bool router_grad_x_tc_ok(int64_t E);
-usaf_status router_grad_x_tc(const RouterGradArgs& a, cudaStream_t st);
+// the same on tensor cores (bf16 x, dx)
+void router_grad_tc_layout(int64_t T, int64_t E, int64_t H, Carver& c, RouterGradWs& w);
+usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& w, cudaStream_t st);
 
 // ---------------------------------------------------------------- 8-bit activation store
 struct Act8Args {
