@@ -98,7 +98,7 @@ constexpr int N = 256;
 constexpr int BOX = 64 * BK * 2;
 constexpr int B_BYTES = 4 * BOX;
 constexpr int FLUSH = 8;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;  // of each 32 lanes by 64 columns
 constexpr int OUT_PITCH = N + 4;  // floats per row of the tile in the epilogue
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 template <bool STACK>
@@ -232,26 +232,22 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
       mbar_drain(done, 0, clock64() + TIMEOUT_CYCLES);
     }
   } else {  // ---------------------------------------------------- epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + half * 128;
-    const int rows = STACK ? 3 * ep : ep;
-    float sum[4][32];  // this lane's row, 128 columns
-    const int nch = q * 32 < rows ? min(4, (nbox * 64 - half * 128) / 32) : 0;
+    const int q = warp & 3, col = (warp - 2) >> 2;  // lanes' quarter, box of columns
+    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + col * 64;
+    const bool mine = q * 32 < (STACK ? 3 * ep : ep) && col < nbox;
+    float sum[2][32];  // this lane's row, 64 columns
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
       for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
     auto add = [&](uint32_t from) {
+      if (!mine) return;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (c >= nch) break;
+        float d[16];
+        tmem_ld16(from + c * 16, d);
 #pragma unroll
-        for (int i = 0; i < 32; i += 16) {
-          float d[16];
-          tmem_ld16(from + c * 32 + i, d);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) sum[c][i + j] += d[j];
-        }
+        for (int j = 0; j < 16; ++j) sum[c / 2][c % 2 * 16 + j] += d[j];
       }
     };
     bool ok = true;
@@ -270,10 +266,10 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
       tc_fence_after();
       if constexpr (!STACK) add(ta + N);
       // registers -> the ring (free after the last MMA), for whole rows of global memory
-      float* tile = reinterpret_cast<float*>(smem) + (q * 32 + lane) * OUT_PITCH + half * 128;
+      float* tile = reinterpret_cast<float*>(smem) + (q * 32 + lane) * OUT_PITCH + col * 64;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= nch) break;
+      for (int c = 0; c < 2; ++c) {
+        if (!mine) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           reinterpret_cast<float4*>(tile + c * 32)[j] = make_float4(
@@ -372,24 +368,32 @@ constexpr int A_PART = TM * KB * 2;
 constexpr int A_BYTES = 2 * A_PART;
 constexpr int B_BLOCK = 2 * 2 * KB * 128;  // w's two parts, two groups of 64 features, KB experts
 constexpr int BOX = TM * 64 * 2;
-constexpr int NA = 2;
 constexpr int MAX_RES = 256;
-constexpr int MAX_SLOTS = 6;
-constexpr int EPI_WARPS = 8;
+constexpr int MAX_NA = 3;
+constexpr int MAX_SLOTS = 8;
+constexpr int EPI_WARPS = 16;  // two boxes of a tile by two tiles by four quarters of lanes
 constexpr int THREADS = 96 + 32 * EPI_WARPS;
 constexpr int SMEM_MAX = 232448;
-__host__ __device__ constexpr int b_bytes(int ke) {  // of the resident parts, or of NA blocks
-  return ke <= MAX_RES ? 2 * 2 * ke * 128 : NA * B_BLOCK;
+// A blocks in the ring
+__host__ __device__ constexpr int ring(int ke) { return ke > 64 && ke <= 128 ? 3 : 2; }
+__host__ __device__ constexpr int b_bytes(int ke) {  // of the resident parts, or of the ring's blocks
+  return ke <= MAX_RES ? 2 * 2 * ke * 128 : ring(ke) * B_BLOCK;
 }
+// Boxes of the staging ring. A wait by parity tells a phase only from its neighbours, so a box's
+// barriers serve one epilogue group, whose tiles use the box in turn: with two groups a box (tiles
+// of either parity) that takes a multiple of four; where fewer fit, one group does all tiles.
 __host__ __device__ constexpr int slots(int ke) {
-  const int s = (SMEM_MAX - 1024 - 512 - NA * A_BYTES - b_bytes(ke)) / BOX;
-  return s < MAX_SLOTS ? s : MAX_SLOTS;
+  const int s = (SMEM_MAX - 1024 - 512 - ring(ke) * A_BYTES - b_bytes(ke)) / BOX;
+  return s >= MAX_SLOTS ? MAX_SLOTS : (s >= 4 ? 4 : 2);
 }
-static_assert(slots(MAX_RES) >= 2 && slots(1024) >= 2, "staging for one tile");
+static_assert(slots(64) == 8 && slots(128) == 4, "two tiles at least");
+static_assert(2 * BOX + ring(MAX_RES) * A_BYTES + b_bytes(MAX_RES) + 1536 <= SMEM_MAX &&
+                  4 * BOX + ring(1024) * A_BYTES + b_bytes(1024) + 1536 <= SMEM_MAX,
+              "one tile at least");
 struct Params {
   int64_t T;
   int E, H, ke;
-  int slots;
+  int ring, slots;
   int per_group;   // CTAs that share a feature group
   int add;         // dx_in is there
   uint32_t* status;
@@ -410,16 +414,17 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  const int ke = p.ke, NS = p.slots;
+  const int ke = p.ke, NS = p.slots, NA = p.ring;
   uint8_t* sA = smem;
   uint8_t* sStage = smem + NA * A_BYTES;
   uint8_t* sB = sStage + NS * BOX;  // [part][feature group of 64][expert][64 features] (a block)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sB + b_bytes(ke));
-  // full[NA], empty[NA], tfull[2], tempty[2], loaded[NS], added[NS], freed[NS], done, wfull
-  const uint32_t full = smem_u32(bars), empty = full + 8 * NA, tfull = empty + 8 * NA,
+  // full[], empty[] of the A ring, tfull[2], tempty[2], loaded[], added[], freed[] of the boxes, done,
+  // wfull
+  const uint32_t full = smem_u32(bars), empty = full + 8 * MAX_NA, tfull = empty + 8 * MAX_NA,
                  tempty = tfull + 16, loaded = tempty + 16, added = loaded + 8 * MAX_SLOTS,
                  freed = added + 8 * MAX_SLOTS, done = freed + 8 * MAX_SLOTS, wfull = done + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NA + 4 + 3 * MAX_SLOTS + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_NA + 4 + 3 * MAX_SLOTS + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr uint32_t COLS = 2 * NH;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (!p.sum) dep_wait();  // else the kernel before is g_router's, which saw the parts written
-  bool bad = false;
+  float odd = 0.f;  // NaN once a produced value was not finite
 
   if (warp == 0) {
     if (lane == 0) {  // ------------------------------------------------ A and B blocks
@@ -555,18 +560,19 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
       }
     }
   } else {  // ---------------------------------------------------- epilogue: add and store
-    const int q = warp & 3, b = (warp - 3) >> 2;  // lanes' quarter, box of the tile
+    // lanes' quarter, box of the tile, tiles of one parity (and so one accumulator)
+    const int q = warp & 3, b = ((warp - 3) >> 2) & 1, par = (warp - 3) >> 3;
+    const int pars = NS >= 4 ? 2 : 1;
     const bool issuer = ((warp - 3) & 3) == 0 && lane == 0;
     const int row = q * 32 + lane;
-    if (b < nbox) {
-      int n = 0;
-      for (int t = first; t < tiles; t += p.per_group, ++n) {
+    if (b < nbox && par < pars) {
+      for (int n = par, t = first + par * p.per_group; t < tiles;
+           t += pars * p.per_group, n += pars) {
         const int u = n * nbox + b, s = u % NS;
         const uint32_t ph = (u / NS) & 1;
         if (!mbar_wait_warp(loaded + 8 * s, ph, abort_flag)) break;
         if (!mbar_wait_warp(tfull + 8 * (n & 1), (n >> 1) & 1, abort_flag)) break;
         tc_fence_after();
-        const bool live = (int64_t)t * TM + row < p.T;
         uint8_t* box = sStage + s * BOX + row * 128;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
               }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) bad |= live && !finite_f(d[8 * c + j]);
+            for (int j = 0; j < 8; ++j) odd = fmaf(d[8 * c + j], 0.f, odd);
             *at = make_uint4(pack_bf16x2(d[8 * c], d[8 * c + 1]),
                              pack_bf16x2(d[8 * c + 2], d[8 * c + 3]),
                              pack_bf16x2(d[8 * c + 4], d[8 * c + 5]),
@@ -615,7 +621,7 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
       __syncwarp();
     }
   }
-  flag_status_warp(p.status, bad, USAF_DEV_NONFINITE);
+  flag_status_warp(p.status, odd != 0.f, USAF_DEV_NONFINITE);
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) flag_status(p.status, USAF_DEV_TIMEOUT);
@@ -650,7 +656,7 @@ usaf_status launch_x(const CUtensorMap& d, const CUtensorMap& w, const CUtensorM
                      const CUtensorMap& out, const gx::Params& p, unsigned grid, cudaStream_t st) {
   USAF_TRACE("router_grad_x", st);
   if (!grow_smem(router_grad_x_tc_kernel<RES>, gx::SMEM_MAX)) return USAF_ERR_CUDA;
-  const int smem = gx::NA * gx::A_BYTES + p.slots * gx::BOX + gx::b_bytes(p.ke) + 1024 + 512;
+  const int smem = p.ring * gx::A_BYTES + p.slots * gx::BOX + gx::b_bytes(p.ke) + 1024 + 512;
   return launch_dep(router_grad_x_tc_kernel<RES>, dim3(grid), gx::THREADS, smem, st, d, w, in, out,
                     p);
 }
@@ -712,6 +718,7 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
   }
   CUtensorMap d, w, in, out;
   const uint32_t wrows = ke <= gx::MAX_RES ? ke : gx::KB;
+  const int64_t groups = ceil_div(H, gx::NH), tiles = ceil_div(a.T, gx::TM);
   if (!map_bf16_2d(&d, parts, 3 * ep, a.T, 64, gx::TM) ||
       !map_bf16_2d(&w, wparts, H, 2 * ke, 64, wrows) ||
       !map_bf16_2d(&out, a.dx, H, a.T, 64, gx::TM) ||
@@ -722,6 +729,7 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
   p.E = E;
   p.H = H;
   p.ke = ke;
+  p.ring = gx::ring(ke);
   p.slots = gx::slots(ke);
   p.add = a.dx_in != nullptr;
   p.status = a.status;
@@ -729,7 +737,6 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
   p.splits = (int)splits;
   p.g_in = a.g_in;
   p.g_router = a.g_router;
-  const int64_t groups = ceil_div(H, gx::NH), tiles = ceil_div(a.T, gx::TM);
   int64_t most = device_sm_count() / groups;
   if (most < 1) most = 1;
   p.per_group = (int)(most < tiles ? most : tiles);

@@ -82,6 +82,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t sr
       "r"(c0), "r"(c1), "r"(src)
       : "memory");
 }
+// `bytes` (a multiple of 16) from shared to global memory, both 16-byte aligned
+__device__ __forceinline__ void bulk_store(void* to, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
