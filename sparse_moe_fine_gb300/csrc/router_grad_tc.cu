@@ -257,13 +257,12 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       add(ta + acc * N);
+      if ((turn + 1) * FLUSH >= nkb) break;  // the last: every MMA is complete
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(given + 8 * acc);
     }
-    if (ok) ok = mbar_wait_warp(done, 0, abort_flag);
-    if (ok && *abort_flag == 0) {
-      tc_fence_after();
+    if (ok) {
       if constexpr (!STACK) add(ta + N);
       // registers -> the ring (free after the last MMA), for whole rows of global memory
       float* tile = reinterpret_cast<float*>(smem) + (q * 32 + lane) * OUT_PITCH + col * 64;
@@ -282,35 +281,45 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
   if (*abort_flag) {
     if (threadIdx.x == 0) flag_status(p.status, USAF_DEV_TIMEOUT);
   } else {
-    const float* tile = reinterpret_cast<const float*>(smem);
+    float* tile = reinterpret_cast<float*>(smem);
     const int ne = min(p.E - e0, 128), w4 = nbox * 16;
-    float* out = p.whole ? p.out : p.out + blockIdx.z * (int64_t)p.E * p.H;
     bool bad = false;
-    for (int i = threadIdx.x; i < ne * w4; i += THREADS) {
-      const int e = i / w4, c = (i - e * w4) * 4;
-      float4 a = *reinterpret_cast<const float4*>(tile + e * OUT_PITCH + c);
-      if constexpr (STACK) {
+    if (STACK || p.whole)
+      for (int i = threadIdx.x; i < ne * w4; i += THREADS) {
+        const int e = i / w4, c = (i - e * w4) * 4;
+        float4 a = *reinterpret_cast<const float4*>(tile + e * OUT_PITCH + c);
+        if constexpr (STACK) {
 #pragma unroll
-        for (int part = 1; part < 3; ++part) {
-          const float4 b =
-              *reinterpret_cast<const float4*>(tile + (e + part * ep) * OUT_PITCH + c);
-          a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+          for (int part = 1; part < 3; ++part) {
+            const float4 b =
+                *reinterpret_cast<const float4*>(tile + (e + part * ep) * OUT_PITCH + c);
+            a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+          }
         }
-      }
-      const int64_t o = (int64_t)(e0 + e) * p.H + h0 + c;
-      float r[4] = {a.x, a.y, a.z, a.w};
-      if (p.whole) {
+        if (!p.whole) {
+          *reinterpret_cast<float4*>(tile + e * OUT_PITCH + c) = a;
+          continue;
+        }
+        const int64_t o = (int64_t)(e0 + e) * p.H + h0 + c;
+        float r[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 4; ++j) {  // g_in and g_router need no alignment
           if (p.g_in) r[j] += p.g_in[o + j];
           bad |= !finite_f(r[j]);
-          out[o + j] = r[j];
+          p.out[o + j] = r[j];
         }
-      } else {
-        *reinterpret_cast<float4*>(out + o) = make_float4(r[0], r[1], r[2], r[3]);
+      }
+    flag_status_warp(p.status, bad, USAF_DEV_NONFINITE);
+    if (!p.whole) {  // rows of the tile by the copy engine
+      fence_async_smem();
+      __syncthreads();
+      if (threadIdx.x < ne) {
+        bulk_store(p.out + blockIdx.z * (int64_t)p.E * p.H + (int64_t)(e0 + threadIdx.x) * p.H + h0,
+                   smem_u32(tile + threadIdx.x * OUT_PITCH), nbox * 256);
+        bulk_commit();
+        bulk_wait();
       }
     }
-    flag_status_warp(p.status, bad, USAF_DEV_NONFINITE);
   }
   __syncthreads();
   if (warp == 1) {
@@ -326,13 +335,14 @@ __device__ __forceinline__ void reduce_parts(const float* part, int splits, int6
   bool bad = false;
   for (int64_t i = i0 * 4; i < count; i += n * 4) {  // count = E H is a multiple of 64
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < splits; s0 += 8) {
-      float4 d[8];
+    constexpr int U = 10;  // loads in flight
+    for (int s0 = 0; s0 < splits; s0 += U) {
+      float4 d[U];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int u = 0; u < U; ++u)
         if (s0 + u < splits) d[u] = __ldcg(reinterpret_cast<const float4*>(part + (s0 + u) * count + i));
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int u = 0; u < U; ++u)
         if (s0 + u < splits) v.x += d[u].x, v.y += d[u].y, v.z += d[u].z, v.w += d[u].w;
     }
     float r[4] = {v.x, v.y, v.z, v.w};
@@ -359,7 +369,8 @@ __global__ void __launch_bounds__(256)
 // for all experts stays in shared memory (at most 256 experts); else it comes through the ring with
 // A. dx_in comes and dx goes by TMA through a ring of 128 x 64 boxes in which the epilogue adds, so
 // token rows are read and written in whole lines while later tiles are on their way.
-// The same launch adds up g_router's stretches at its end (`sum`), which saves one of its own.
+// The same launch adds up g_router's stretches (`sum`): its epilogue warps do so while the first
+// tiles are on their way, which saves a launch and hides most of the sum.
 namespace gx {
 constexpr int TM = 128;      // tokens of a tile
 constexpr int NH = 128;      // features of a CTA
@@ -565,6 +576,13 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
     const int pars = NS >= 4 ? 2 : 1;
     const bool issuer = ((warp - 3) & 3) == 0 && lane == 0;
     const int row = q * 32 + lane;
+    if (p.sum) {
+      dep_wait();  // every stretch's sums are there
+      constexpr int N = 32 * EPI_WARPS;
+      reduce_parts(p.sum, p.splits, (int64_t)p.E * p.H, p.g_in, p.g_router, p.status,
+                   (int64_t)blockIdx.x * N + threadIdx.x - 96, (int64_t)gridDim.x * N);
+      __syncwarp();
+    }
     if (b < nbox && par < pars) {
       for (int n = par, t = first + par * p.per_group; t < tiles;
            t += pars * p.per_group, n += pars) {
@@ -628,11 +646,6 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_free(tmem, COLS);
-  }
-  if (p.sum) {
-    dep_wait();  // every stretch's sums are there
-    reduce_parts(p.sum, p.splits, (int64_t)p.E * p.H, p.g_in, p.g_router, p.status,
-                 (int64_t)blockIdx.x * THREADS + threadIdx.x, (int64_t)gridDim.x * THREADS);
   }
 }
 
