@@ -91,7 +91,8 @@ usaf_status usaf_router_aux_bwd(int64_t T, int64_t E, int64_t k, const float* lo
  * of bf16 layers; their order is fixed. The workspace and, of bf16 layers, x, dx_in, dx and
  * w_router must be 16-byte aligned (INVALID_ARG otherwise).
  * Limits: T >= 1, 1 <= E <= 1024, H >= 1, T < 2^31 - 65536, E*H < 2^31.
- * Errors: INVALID_ARG, UNSUPPORTED (bf16 with H % 64 != 0), WORKSPACE, CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (bf16 with H % 64 != 0; fp32 beyond 2^31 tiles of 64 x 64),
+ * WORKSPACE, CUDA.
  * ------------------------------------------------------------------------------------------- */
 size_t usaf_router_grad_workspace_size(int64_t T, int64_t E, int64_t H, usaf_dtype dtype);
 usaf_status usaf_router_grad(int64_t T, int64_t E, int64_t H, usaf_dtype dtype,
