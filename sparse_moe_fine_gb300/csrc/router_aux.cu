@@ -87,6 +87,26 @@ struct Groups {
     }
     return lo - 1 < p.G ? lo - 1 : -1;
   }
+  // the first group that ends after token t, G if none does
+  __device__ __forceinline__ int first_ending_after(int64_t t) const {
+    int lo = 0, hi = p.G;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (at(mid + 1) <= t) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo;
+  }
+  // the last group that starts before token t, -1 if none does
+  __device__ __forceinline__ int last_starting_before(int64_t t) const {
+    int lo = 0, hi = p.G;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (at(mid) < t) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo - 1;
+  }
 };
 
 template <int LPR>
@@ -172,8 +192,10 @@ __device__ __forceinline__ void write_loss(const AuxParams& p, double bal, doubl
   if (!finite_f(b) || !finite_f(zz)) flag_status(p.status, USAF_DEV_NONFINITE);
 }
 
-// One block per chunk of tokens. Per (chunk, group) that meet: the warps' rows are summed in
-// registers, then over rows of a warp and over the warps in a fixed order.
+// One block per chunk of tokens; its sums go to a slot per group that the chunk meets. One or two
+// groups: the block's warps share each group's rows, summed in registers, then over the rows of a
+// warp and over the warps in a fixed order. More (short packed sequences): each warp takes groups of
+// its own, so that no barrier stands between them.
 // ONE: the only chunk; the block also forms the outputs and the loss (one launch).
 template <int LPR, int NV, bool VEC, bool ONE>
 __global__ void __launch_bounds__(AUX_THREADS)
@@ -184,15 +206,16 @@ __global__ void __launch_bounds__(AUX_THREADS)
   float* s_prob = sm;                                                   // [AUX_WARPS][E]
   int32_t* s_cnt = reinterpret_cast<int32_t*>(sm + AUX_WARPS * p.E);    // [E]
   uint8_t* s_live = reinterpret_cast<uint8_t*>(s_cnt + p.E);            // [chunk]
+  __shared__ int32_t s_off[OFF_CAP];
   __shared__ float s_z[AUX_WARPS];
   __shared__ int s_n[AUX_WARPS];
-  __shared__ double s_red[AUX_THREADS];
+  __shared__ double s_bal[AUX_WARPS], s_za[AUX_WARPS];
+  __shared__ int64_t s_na[AUX_WARPS];
   constexpr int RPW = 32 / LPR, U = ROWS<NV>, PRE = 4;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int sub = lane % LPR, rw = lane / LPR;
   const int64_t t0 = (int64_t)blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
   dep_launch();
-  __shared__ int32_t s_off[OFF_CAP];
   const Groups groups(p, s_off);
   for (int e = threadIdx.x; e < p.E; e += AUX_THREADS) s_cnt[e] = 0;
   if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *w.arrived = 0;  // for the final kernel
@@ -203,42 +226,32 @@ __global__ void __launch_bounds__(AUX_THREADS)
     }
     for (int i = threadIdx.x; i < p.G; i += AUX_THREADS) n_out[i] = 0;
   }
-  double bal_all = 0.0, z_all = 0.0;  // ONE: of this thread's experts / of thread 0
+  double bal_all = 0.0, z_all = 0.0;  // ONE: this thread's share of the loss
   int64_t n_all = 0;
   bool badidx = false;
   __syncthreads();
-  int64_t t = t0;
-  while (t < t1) {
-    const int g = groups.of(t);
-    if (g < 0) {  // before the first group or behind the last
-      const int64_t f = groups.at(0);
-      t = f > t ? f : t1;
-      continue;
-    }
-    int64_t te = min(t1, groups.at(g + 1));
-    if (te <= t) te = t + 1;  // only where the offsets decrease
-    __syncthreads();  // the last segment's counts are out; ONE: the zeroed outputs too
-    // the segment's first expert indices, on their way while the rows are read
-    const int64_t q0 = t * p.k + threadIdx.x, q1 = te * p.k;
-    int ids[PRE];
-#pragma unroll
-    for (int u = 0; u < PRE; ++u)
-      ids[u] = q0 + u * AUX_THREADS < q1 ? p.topk[q0 + u * AUX_THREADS] : 0;
-    float acc[NV];
+  const int g0 = groups.first_ending_after(t0), g1 = groups.last_starting_before(t1);
+  const bool alone = g1 - g0 >= 2;  // a warp on its own takes a group
+
+  // Rows base, base + step, ... below te: sums of this lane's experts, of the squared logsumexps and
+  // of the tokens that take part, whose flags go to s_live.
+  float acc[NV], z;
+  int n;
+  auto rows = [&](int64_t base, int64_t te, int step) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) acc[i] = 0.f;
-    float z = 0.f;
-    int n = 0;
-    for (int64_t base = t + wid * RPW; base < te; base += AUX_WARPS * RPW * U) {
+    z = 0.f;
+    n = 0;
+    for (; base < te; base += step * U) {
       float v[U][NV];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t tok = base + u * AUX_WARPS * RPW + rw;
+        const int64_t tok = base + u * step + rw;
         load_row<LPR, NV, VEC>(p, tok, tok < te, sub, v[u]);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t tok = base + u * AUX_WARPS * RPW + rw;
+        const int64_t tok = base + u * step + rw;
         float lse;
         const bool alive = row_softmax<LPR, NV>(v[u], lse);
 #pragma unroll
@@ -257,69 +270,123 @@ __global__ void __launch_bounds__(AUX_THREADS)
     z = row_sum<32>(z);
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (rw == 0) {
+  };
+  auto add = [&](int32_t* cnt, int64_t q, int e) {  // slot q went to expert e
+    if (!s_live[(int)(q - t0 * p.k) / p.k]) return;
+    if (e >= 0 && e < p.E) atomicAdd(&cnt[e], 1);
+    else badidx = true;
+  };
+  float* po = ONE ? prob_out : w.prob;
+  int32_t* co = ONE ? count_out : w.count;
+  auto totals = [&](int g, int64_t slot, int ng, float zg) {
+    if constexpr (ONE) {
+      n_out[g] = ng;
+      n_all += ng;
+      z_all += zg;
+    } else {
+      w.n[slot] = ng;
+      w.z[slot] = zg;
+    }
+  };
+
+  if (alone) {
+    int32_t* cnt = reinterpret_cast<int32_t*>(s_prob) + wid * p.E;
+    for (int e = lane; e < p.E; e += 32) cnt[e] = 0;
+    for (int g = g0 + wid; g <= g1; g += AUX_WARPS) {
+      const int64_t t = max(t0, groups.at(g)), te = min(t1, groups.at(g + 1));
+      if (te <= t) continue;
+      const int64_t slot = ONE ? g : (int64_t)blockIdx.x + g;
+      rows(t, te, RPW);
+      __syncwarp();  // the flags are set, the counts clear
+      for (int64_t q = t * p.k + lane; q < te * p.k; q += 32) add(cnt, q, p.topk[q]);
+      __syncwarp();
+      if (rw == 0) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = expert<LPR, NV>(sub, i);
-        if (e < p.E) s_prob[wid * p.E + e] = acc[i];
+        for (int i = 0; i < NV; ++i) {
+          const int e = expert<LPR, NV>(sub, i);
+          if (e >= p.E) continue;
+          const int c = cnt[e];
+          cnt[e] = 0;
+          po[slot * p.E + e] = acc[i];
+          co[slot * p.E + e] = c;
+          if (ONE && n > 0) bal_all += (double)((float)c * acc[i]) / n;
+        }
       }
+      if (lane == 0) totals(g, slot, n, z);
+      __syncwarp();
     }
-    if (lane == 0) {
-      s_z[wid] = z;
-      s_n[wid] = n;
-    }
-    __syncthreads();
-    // the experts that the segment's live tokens went to
-    auto add = [&](int64_t q, int e) {
-      if (!s_live[(int)(q - t0 * p.k) / p.k]) return;
-      if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
-      else badidx = true;
-    };
+  } else {
+    for (int g = g0; g <= g1; ++g) {
+      const int64_t t = max(t0, groups.at(g)), te = min(t1, groups.at(g + 1));
+      if (te <= t) continue;
+      const int64_t slot = ONE ? g : (int64_t)blockIdx.x + g;
+      // the group's first expert indices, on their way while the rows are read
+      const int64_t q0 = t * p.k + threadIdx.x, q1 = te * p.k;
+      int ids[PRE];
 #pragma unroll
-    for (int u = 0; u < PRE; ++u)
-      if (q0 + u * AUX_THREADS < q1) add(q0 + u * AUX_THREADS, ids[u]);
-    for (int64_t q = q0 + PRE * AUX_THREADS; q < q1; q += AUX_THREADS) add(q, p.topk[q]);
-    __syncthreads();
-    const int64_t slot = ONE ? g : (int64_t)blockIdx.x + g;
-    float* po = ONE ? prob_out : w.prob;
-    int32_t* co = ONE ? count_out : w.count;
-    int ng = 0;
+      for (int u = 0; u < PRE; ++u)
+        ids[u] = q0 + u * AUX_THREADS < q1 ? p.topk[q0 + u * AUX_THREADS] : 0;
+      rows(t + wid * RPW, te, AUX_WARPS * RPW);
+      if (rw == 0) {
 #pragma unroll
-    for (int u = 0; u < AUX_WARPS; ++u) ng += s_n[u];
-    for (int e = threadIdx.x; e < p.E; e += AUX_THREADS) {
-      float s = 0.f;
-#pragma unroll
-      for (int u = 0; u < AUX_WARPS; ++u) s += s_prob[u * p.E + e];
-      const int c = s_cnt[e];
-      s_cnt[e] = 0;
-      po[slot * p.E + e] = s;
-      co[slot * p.E + e] = c;
-      if (ONE && ng > 0) bal_all += (double)((float)c * s) / ng;
-    }
-    if (threadIdx.x == 0) {
-      float s = 0.f;
-#pragma unroll
-      for (int u = 0; u < AUX_WARPS; ++u) s += s_z[u];
-      if constexpr (ONE) {
-        n_out[g] = ng;
-        n_all += ng;
-        z_all += s;
-      } else {
-        w.n[slot] = ng;
-        w.z[slot] = s;
+        for (int i = 0; i < NV; ++i) {
+          const int e = expert<LPR, NV>(sub, i);
+          if (e < p.E) s_prob[wid * p.E + e] = acc[i];
+        }
       }
+      if (lane == 0) {
+        s_z[wid] = z;
+        s_n[wid] = n;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < PRE; ++u)
+        if (q0 + u * AUX_THREADS < q1) add(s_cnt, q0 + u * AUX_THREADS, ids[u]);
+      for (int64_t q = q0 + PRE * AUX_THREADS; q < q1; q += AUX_THREADS) add(s_cnt, q, p.topk[q]);
+      __syncthreads();
+      int ng = 0;
+#pragma unroll
+      for (int u = 0; u < AUX_WARPS; ++u) ng += s_n[u];
+      for (int e = threadIdx.x; e < p.E; e += AUX_THREADS) {
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < AUX_WARPS; ++u) s += s_prob[u * p.E + e];
+        const int c = s_cnt[e];
+        s_cnt[e] = 0;
+        po[slot * p.E + e] = s;
+        co[slot * p.E + e] = c;
+        if (ONE && ng > 0) bal_all += (double)((float)c * s) / ng;
+      }
+      if (threadIdx.x == 0) {
+        float s = 0.f;
+#pragma unroll
+        for (int u = 0; u < AUX_WARPS; ++u) s += s_z[u];
+        totals(g, slot, ng, s);
+      }
+      __syncthreads();  // the shared sums are read
     }
-    t = te;
   }
   if (badidx) flag_status(p.status, USAF_DEV_BAD_INDEX);
   if constexpr (ONE) {
-    s_red[threadIdx.x] = bal_all;
-    __syncthreads();
-    for (int h = AUX_THREADS / 2; h; h >>= 1) {
-      if (threadIdx.x < h) s_red[threadIdx.x] += s_red[threadIdx.x + h];
-      __syncthreads();
+    for (int o = 16; o; o >>= 1) {
+      bal_all += __shfl_xor_sync(0xffffffffu, bal_all, o);
+      z_all += __shfl_xor_sync(0xffffffffu, z_all, o);
+      n_all += __shfl_xor_sync(0xffffffffu, n_all, o);
     }
-    if (threadIdx.x == 0) write_loss(p, s_red[0], z_all, n_all, loss);
+    if (lane == 0) {
+      s_bal[wid] = bal_all;
+      s_za[wid] = z_all;
+      s_na[wid] = n_all;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int u = 1; u < AUX_WARPS; ++u) {
+        bal_all += s_bal[u];
+        z_all += s_za[u];
+        n_all += s_na[u];
+      }
+      write_loss(p, bal_all, z_all, n_all, loss);
+    }
   }
 }
 
