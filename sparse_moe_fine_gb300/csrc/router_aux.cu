@@ -180,11 +180,13 @@ __device__ __forceinline__ void load_row(const AuxParams& p, int64_t t, bool in,
   for (int i = 0; i < NV; ++i) v[i] = keep ? v[i] : -INFINITY;
 }
 
-__device__ __forceinline__ void write_loss(const AuxParams& p, double bal, double z, int64_t n,
+// The loss from the sums over groups and experts. fp32: the sums are of positive terms (a double
+// costs this GPU 64 times a float, and a division in doubles was once a third of a small call).
+__device__ __forceinline__ void write_loss(const AuxParams& p, float bal, float z, int64_t n,
                                            float* loss) {
-  const double inv = n > 0 ? 1.0 / (double)n : 0.0;
-  const float b = n > 0 ? (float)((double)p.share * inv * bal) : 0.f;
-  const float zz = n > 0 ? (float)(inv * z) : 0.f;
+  const float inv = n > 0 ? 1.f / (float)n : 0.f;
+  const float b = n > 0 ? p.share * inv * bal : 0.f;
+  const float zz = n > 0 ? inv * z : 0.f;
   const float tot = (p.coef_b != 0.f ? p.coef_b * b : 0.f) + (p.coef_z != 0.f ? p.coef_z * zz : 0.f);
   loss[0] = tot;
   loss[1] = b;
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(AUX_THREADS)
   __shared__ int32_t s_off[OFF_CAP];
   __shared__ float s_z[AUX_WARPS];
   __shared__ int s_n[AUX_WARPS];
-  __shared__ double s_bal[AUX_WARPS], s_za[AUX_WARPS];
+  __shared__ float s_bal[AUX_WARPS], s_za[AUX_WARPS];
   __shared__ int64_t s_na[AUX_WARPS];
   constexpr int RPW = 32 / LPR, U = ROWS<NV>, PRE = 4;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(AUX_THREADS)
     }
     for (int i = threadIdx.x; i < p.G; i += AUX_THREADS) n_out[i] = 0;
   }
-  double bal_all = 0.0, z_all = 0.0;  // ONE: this thread's share of the loss
+  float bal_all = 0.f, z_all = 0.f;  // ONE: this thread's share of the loss
   int64_t n_all = 0;
   bool badidx = false;
   __syncthreads();
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(AUX_THREADS)
           cnt[e] = 0;
           po[slot * p.E + e] = acc[i];
           co[slot * p.E + e] = c;
-          if (ONE && n > 0) bal_all += (double)((float)c * acc[i]) / n;
+          if (ONE && n > 0) bal_all += (float)c * acc[i] / (float)n;
         }
       }
       if (lane == 0) totals(g, slot, n, z);
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(AUX_THREADS)
         s_cnt[e] = 0;
         po[slot * p.E + e] = s;
         co[slot * p.E + e] = c;
-        if (ONE && ng > 0) bal_all += (double)((float)c * s) / ng;
+        if (ONE && ng > 0) bal_all += (float)c * s / (float)ng;
       }
       if (threadIdx.x == 0) {
         float s = 0.f;
@@ -439,11 +441,11 @@ __global__ void __launch_bounds__(FIN_THREADS)
       n += s_n[u];
       z += s_z[u];
     }
-    double bal = 0.0;
+    float bal = 0.f;
     if (e < p.E) {
       prob[(int64_t)g * p.E + e] = a;
       count[(int64_t)g * p.E + e] = c;
-      if (n > 0) bal = (double)((float)c * a) / n;
+      if (n > 0) bal = (float)c * a / (float)n;
     }
     for (int o = 16; o; o >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, o);
     if (lane == 0) {
@@ -460,9 +462,9 @@ __global__ void __launch_bounds__(FIN_THREADS)
   if (!s_last) return;
   __threadfence();
   // fixed order: thread t its share of the blocks and groups, then a tree
-  __shared__ double r_b[FIN_WARPS], r_z[FIN_WARPS];
+  __shared__ float r_b[FIN_WARPS], r_z[FIN_WARPS];
   __shared__ int64_t r_n[FIN_WARPS];
-  double sb = 0.0, sz = 0.0;
+  float sb = 0.f, sz = 0.f;
   int64_t sn = 0;
   for (int64_t i = threadIdx.x; i < gridDim.x; i += FIN_THREADS) sb += __ldcg(w.bal + i);
   for (int i = threadIdx.x; i < p.G; i += FIN_THREADS) {
@@ -662,7 +664,7 @@ void aux_ws_layout(int64_t T, int64_t E, int64_t G, Carver& c, AuxWs& w) {
   w.count = c.take<int32_t>(slots * E);
   w.n = c.take<int32_t>(slots);
   w.z = c.take<float>(slots);
-  w.bal = c.take<double>(G * ceil_div(E, 32));
+  w.bal = c.take<float>(G * ceil_div(E, 32));
   w.group_z = c.take<float>(G);
   w.arrived = c.take<uint32_t>(1);
 }

@@ -51,7 +51,7 @@ struct AuxWs {
   int32_t* count;
   int32_t* n;  // [slots]
   float* z;
-  double* bal;        // [G][ceil(E / 32)] shares of the balance sum
+  float* bal;         // [G][ceil(E / 32)] shares of the balance sum
   float* group_z;     // [G]
   uint32_t* arrived;  // blocks of the final kernel that are done
 };
