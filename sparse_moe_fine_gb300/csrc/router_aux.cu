@@ -16,7 +16,7 @@ namespace {
 
 constexpr int AUX_WARPS = 8;
 constexpr int AUX_THREADS = 32 * AUX_WARPS;
-constexpr int FIN_WARPS = 32;   // slot lanes of a final block, 32 experts wide
+constexpr int FIN_WARPS = 32;
 constexpr int FIN_THREADS = 32 * FIN_WARPS;
 // Rows that a lane has in flight: 16 values at most.
 template <int NV>
@@ -392,77 +392,97 @@ __global__ void __launch_bounds__(AUX_THREADS)
   }
 }
 
-// Sums the chunks' partials of 32 experts of a group: lanes are experts, warps share the chunks.
-// The block that arrives last (a counter that the partials' kernel cleared) adds the blocks'
-// shares of the loss in their order.
+// Sums the chunks' partials of `el` experts of a group: threads are (slot lane, expert). Where there
+// are several blocks, the one that arrives last (a counter that the partials' kernel cleared) adds the
+// blocks' shares of the loss in their order.
 __global__ void __launch_bounds__(FIN_THREADS)
-    aux_final_kernel(const AuxParams p, AuxWs w, int nb, int32_t* __restrict__ count,
+    aux_final_kernel(const AuxParams p, AuxWs w, int el, int nb, int32_t* __restrict__ count,
                      float* __restrict__ prob, int32_t* __restrict__ n_tok,
                      float* __restrict__ loss) {
-  __shared__ float s_p[FIN_WARPS][33], s_z[FIN_WARPS];
-  __shared__ int32_t s_c[FIN_WARPS][33], s_n[FIN_WARPS];
+  __shared__ float s_p[FIN_THREADS], s_z[FIN_WARPS], s_b[FIN_WARPS];
+  __shared__ int32_t s_c[FIN_THREADS], s_n[FIN_WARPS];
   __shared__ bool s_last;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int g = blockIdx.x / nb, eb = blockIdx.x % nb, e = eb * 32 + lane;
+  const int tx = threadIdx.x % el, ls = threadIdx.x / el, sl = FIN_THREADS / el;
+  const int g = blockIdx.x / nb, eb = blockIdx.x % nb, e = eb * el + tx;
   float a = 0.f, z = 0.f;
   int32_t c = 0, n = 0;
   const int64_t o0 = clamp_off(p, g), o1 = clamp_off(p, g + 1);
+  const int64_t ch0 = o0 / p.chunk, ch1 = o1 > o0 ? (o1 - 1) / p.chunk : ch0 - 1;
   dep_launch();
   dep_wait();
-  if (o1 > o0) {
-    const int64_t ch1 = (o1 - 1) / p.chunk;
+  if (e < p.E) {
+    const float* pp = w.prob + (ch0 + ls + g) * p.E + e;
+    const int32_t* pc = w.count + (ch0 + ls + g) * p.E + e;
 #pragma unroll 8
-    for (int64_t ch = o0 / p.chunk + wid; ch <= ch1; ch += FIN_WARPS) {
-      const int64_t slot = ch + g;
-      if (e < p.E) {
-        a += w.prob[slot * p.E + e];
-        c += w.count[slot * p.E + e];
-      }
-      if (lane == 0) {
-        n += w.n[slot];
-        z += w.z[slot];
-      }
+    for (int64_t ch = ch0 + ls; ch <= ch1; ch += sl, pp += (int64_t)sl * p.E, pc += (int64_t)sl * p.E) {
+      a += *pp;
+      c += *pc;
     }
   }
-  s_p[wid][lane] = a;
-  s_c[wid][lane] = c;
+  for (int64_t ch = ch0 + threadIdx.x; ch <= ch1; ch += FIN_THREADS) {
+    n += w.n[ch + g];
+    z += w.z[ch + g];
+  }
+  s_p[threadIdx.x] = a;
+  s_c[threadIdx.x] = c;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
   if (lane == 0) {
     s_n[wid] = n;
     s_z[wid] = z;
   }
   __syncthreads();
-  if (wid == 0) {
-    a = z = 0.f;
-    c = n = 0;
-#pragma unroll 8
-    for (int u = 0; u < FIN_WARPS; ++u) {
-      a += s_p[u][lane];
-      c += s_c[u][lane];
-      n += s_n[u];
-      z += s_z[u];
+  // every warp needs the group's tokens; warps of slot lane 0 add the lanes
+  n = s_n[lane];
+  z = s_z[lane];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  float bal = 0.f;
+  if (ls == 0) {
+    for (int u = 1; u < sl; ++u) {
+      a += s_p[u * el + tx];
+      c += s_c[u * el + tx];
     }
-    float bal = 0.f;
     if (e < p.E) {
       prob[(int64_t)g * p.E + e] = a;
       count[(int64_t)g * p.E + e] = c;
       if (n > 0) bal = (float)c * a / (float)n;
     }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, o);
+  if (lane == 0) s_b[wid] = bal;
+  __syncthreads();
+  if (wid != 0) {
+    if (gridDim.x == 1) return;
+  } else {
+    bal = s_b[lane];
+#pragma unroll
     for (int o = 16; o; o >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, o);
     if (lane == 0) {
-      w.bal[blockIdx.x] = bal;
-      if (eb == 0) {
-        n_tok[g] = n;
-        w.group_z[g] = z;
+      if (eb == 0) n_tok[g] = n;
+      if (gridDim.x == 1) {
+        write_loss(p, bal, z, n, loss);
+      } else {
+        w.bal[blockIdx.x] = bal;
+        if (eb == 0) w.group_z[g] = z;
+        __threadfence();
+        s_last = atomicAdd(w.arrived, 1u) == gridDim.x - 1;
       }
-      __threadfence();
-      s_last = atomicAdd(w.arrived, 1u) == gridDim.x - 1;
     }
+    if (gridDim.x == 1) return;
   }
   __syncthreads();
   if (!s_last) return;
   __threadfence();
   // fixed order: thread t its share of the blocks and groups, then a tree
-  __shared__ float r_b[FIN_WARPS], r_z[FIN_WARPS];
   __shared__ int64_t r_n[FIN_WARPS];
   float sb = 0.f, sz = 0.f;
   int64_t sn = 0;
@@ -472,6 +492,7 @@ __global__ void __launch_bounds__(FIN_THREADS)
     sn += __ldcg(n_tok + i);
   }
   auto tree = [&] {
+#pragma unroll
     for (int o = 16; o; o >>= 1) {
       sb += __shfl_xor_sync(0xffffffffu, sb, o);
       sz += __shfl_xor_sync(0xffffffffu, sz, o);
@@ -480,14 +501,14 @@ __global__ void __launch_bounds__(FIN_THREADS)
   };
   tree();
   if (lane == 0) {
-    r_b[wid] = sb;
-    r_z[wid] = sz;
+    s_b[wid] = sb;
+    s_z[wid] = sz;
     r_n[wid] = sn;
   }
   __syncthreads();
   if (wid != 0) return;
-  sb = r_b[lane];
-  sz = r_z[lane];
+  sb = s_b[lane];
+  sz = s_z[lane];
   sn = r_n[lane];
   tree();
   if (lane == 0) write_loss(p, sb, sz, sn, loss);
@@ -690,8 +711,11 @@ usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, in
   }));
   if (one) return USAF_OK;
   USAF_TRACE("router_aux_final", st);
-  const int nb = (int)ceil_div(a.E, 32);  // blocks of a group
-  return launch_dep(aux_final_kernel, dim3((unsigned)(nb * a.G)), FIN_THREADS, 0, st, p, w, nb,
+  // experts of a block: all of a common router's at once while that leaves a thread at most 20 chunks
+  // (a batch of 4,096 tokens then needs one block and no counter), else fewer and more chunk lanes
+  const int el = ceil_div(p.nchunks, a.G) <= 160 && a.E > 32 ? 128 : 32;
+  const int nb = (int)ceil_div(a.E, el);
+  return launch_dep(aux_final_kernel, dim3((unsigned)(nb * a.G)), FIN_THREADS, 0, st, p, w, el, nb,
                     count, prob_sum, n_tok, loss);
 }
 
