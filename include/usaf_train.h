@@ -122,7 +122,8 @@ usaf_status usaf_router_grad(int64_t T, int64_t E, int64_t H, usaf_dtype dtype,
  *   rows come out 0 (in h and wa unless their block is NaN); of the rows past expert_offset[E],
  *   x_perm's are 0 and those of h and wa may be left as they were, as after a forward.
  * All pointers of the store and the tensors, perm_tok and perm_slot must be 16-byte aligned.
- * Any T, H, E, k, I of a valid shape, both dtypes. Errors: INVALID_ARG, CUDA.
+ * Any T, H, E, k, I of a valid shape, both dtypes.
+ * Errors: INVALID_ARG, UNSUPPORTED (a restore beyond 2^31 blocks of work), CUDA.
  * ------------------------------------------------------------------------------------------- */
 #define USAF_ACT8_BLOCK 16
 usaf_status usaf_act8_save(const usaf_moe_shape* shape, usaf_dtype dtype, const void* x,

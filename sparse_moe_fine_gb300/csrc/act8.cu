@@ -498,9 +498,12 @@ usaf_status restore(const Act8Args& a, void* x_out, void* x_perm, void* h, void*
     if constexpr (sizeof(T) == 2) {
       if (tiles) {
         // four blocks' tiles per SM; the rest of the shared memory stays L1
-        if (cudaFuncSetAttribute(act8_restore_kernel<T, true>,
-                                 cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 66) != cudaSuccess)
+        static OncePerDevice once;
+        if (!once([] {
+              return cudaFuncSetAttribute(act8_restore_kernel<T, true>,
+                                          cudaFuncAttributePreferredSharedMemoryCarveout,
+                                          66) == cudaSuccess;
+            }))
           return USAF_ERR_CUDA;
         act8_restore_kernel<T, true><<<(unsigned)blocks, THREADS, G_SMEM, st>>>(tm, a, g, xo, ho,
                                                                                 wo);

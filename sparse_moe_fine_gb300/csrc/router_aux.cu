@@ -21,6 +21,11 @@ constexpr int FIN_THREADS = 32 * FIN_WARPS;
 // Rows that a lane has in flight: 16 values at most.
 template <int NV>
 constexpr int ROWS = NV <= 4 ? 4 : (NV <= 8 ? 2 : 1);
+constexpr int MAX_CHUNK = 8192;  // a token's flag is a byte of shared memory
+// Blocks of an SM: four (64 registers a thread) hold the chunks of 16,383 tokens in one wave, where
+// the compiler's own choice needs two (28.7 -> 26.7 us); 32 values a lane need the registers.
+template <int NV>
+constexpr int BLOCKS = NV <= 16 ? 4 : 2;
 // The expert of a lane's i-th value: four neighbours at a time, whether or not the rows' alignment
 // lets them be read as one vector, so that sums have one order and results do not depend on strides.
 template <int LPR, int NV>
@@ -200,7 +205,7 @@ __device__ __forceinline__ void write_loss(const AuxParams& p, float bal, float 
 // its own, so that no barrier stands between them.
 // ONE: the only chunk; the block also forms the outputs and the loss (one launch).
 template <int LPR, int NV, bool VEC, bool ONE>
-__global__ void __launch_bounds__(AUX_THREADS)
+__global__ void __launch_bounds__(AUX_THREADS, BLOCKS<NV>)
     aux_part_kernel(const AuxParams p, AuxWs w, int32_t* __restrict__ count_out,
                     float* __restrict__ prob_out, int32_t* __restrict__ n_out,
                     float* __restrict__ loss) {
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(FIN_THREADS)
 
 // The gradient: each row is read once, its group's counts stay in registers while the group lasts.
 template <int LPR, int NV, bool VEC>
-__global__ void __launch_bounds__(AUX_THREADS)
+__global__ void __launch_bounds__(AUX_THREADS, BLOCKS<NV>)
     aux_bwd_kernel(const AuxParams p, const int32_t* __restrict__ count,
                    const int32_t* __restrict__ n_tok, const float* __restrict__ d_loss, float* out,
                    int64_t ld_out, int accumulate, int rows_per_lane) {
@@ -676,7 +681,7 @@ int64_t aux_chunk_tokens(int64_t T, int64_t E) {
   const int64_t rows = E <= 128 ? 4 : (E <= 256 ? 2 : 1);  // of a warp at a time
   if (T <= 4 * AUX_WARPS * rows) return T;
   const int64_t c = round_up(ceil_div(T, 4 * 152), 32);
-  return c < 32 ? 32 : c;
+  return c < 32 ? 32 : (c > MAX_CHUNK ? MAX_CHUNK : c);
 }
 
 void aux_ws_layout(int64_t T, int64_t E, int64_t G, Carver& c, AuxWs& w) {
@@ -693,15 +698,11 @@ void aux_ws_layout(int64_t T, int64_t E, int64_t G, Carver& c, AuxWs& w) {
 usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, int32_t* n_tok,
                            float* loss, const AuxWs& w, cudaStream_t st) {
   const AuxParams p = make_params(a);
-  const size_t smem = (size_t)(AUX_WARPS + 1) * a.E * 4 + p.chunk;
+  const size_t smem = (size_t)(AUX_WARPS + 1) * a.E * 4 + p.chunk;  // at most 45 KB
   const bool one = p.nchunks == 1;
   USAF_TRY(by_width(a.E, rows_vec(a.logits, a.ld, a.E), [&](auto lpr, auto nv, auto vec) {
     USAF_TRACE("router_aux_part", st);
     auto go = [&](auto kernel) {
-      if (smem > 48 * 1024 &&
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-              cudaSuccess)
-        return USAF_ERR_CUDA;
       kernel<<<p.nchunks, AUX_THREADS, smem, st>>>(p, w, count, prob_sum, n_tok, loss);
       USAF_CHECK_LAUNCH();
       return USAF_OK;

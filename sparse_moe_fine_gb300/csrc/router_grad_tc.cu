@@ -650,9 +650,11 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
 }
 
 template <class K>
-bool grow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
-         cudaSuccess;
+bool grow_smem(OncePerDevice& once, K kernel, int bytes) {
+  return once([&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+           cudaSuccess;
+  });
 }
 
 template <bool STACK>
@@ -660,7 +662,8 @@ usaf_status launch_w(const CUtensorMap& d, const CUtensorMap& x, const gw::Param
                      cudaStream_t st) {
   USAF_TRACE("router_grad_w", st);
   using C = gw::Cfg<STACK>;
-  if (!grow_smem(router_grad_w_tc_kernel<STACK>, C::SMEM)) return USAF_ERR_CUDA;
+  static OncePerDevice once;
+  if (!grow_smem(once, router_grad_w_tc_kernel<STACK>, C::SMEM)) return USAF_ERR_CUDA;
   return launch_dep(router_grad_w_tc_kernel<STACK>, grid, gw::THREADS, C::SMEM, st, d, x, p);
 }
 
@@ -668,7 +671,8 @@ template <bool RES>
 usaf_status launch_x(const CUtensorMap& d, const CUtensorMap& w, const CUtensorMap& in,
                      const CUtensorMap& out, const gx::Params& p, unsigned grid, cudaStream_t st) {
   USAF_TRACE("router_grad_x", st);
-  if (!grow_smem(router_grad_x_tc_kernel<RES>, gx::SMEM_MAX)) return USAF_ERR_CUDA;
+  static OncePerDevice once;
+  if (!grow_smem(once, router_grad_x_tc_kernel<RES>, gx::SMEM_MAX)) return USAF_ERR_CUDA;
   const int smem = p.ring * gx::A_BYTES + p.slots * gx::BOX + gx::b_bytes(p.ke) + 1024 + 512;
   return launch_dep(router_grad_x_tc_kernel<RES>, dim3(grid), gx::THREADS, smem, st, d, w, in, out,
                     p);

@@ -1,6 +1,8 @@
 // Internal launch interfaces of the calls declared in usaf_train.h.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "usaf_train.h"
 
@@ -32,6 +34,23 @@ usaf_status launch_dep(void (*kernel)(P...), dim3 grid, unsigned threads, size_t
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? USAF_OK
                                                                                   : USAF_ERR_CUDA;
 }
+
+// Runs set() once for each device that is current when it is called (a kernel's attributes belong to
+// a device; setting them again costs a small call about a microsecond). set() returns success; one
+// that failed is tried again by the next call. One variable of this type per kernel.
+struct OncePerDevice {
+  std::atomic<uint64_t> done{0};
+  template <class F>
+  bool operator()(F set) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (!set()) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+  }
+};
 
 // ---------------------------------------------------------------- router auxiliary losses
 struct AuxArgs {
