@@ -18,8 +18,28 @@ using namespace tcx;
 
 namespace {
 
-// Part q of the E experts' logits starts at column q * part_cols(E) of a row of three parts.
+// How the parts lie in memory. Routers of at most 40 experts: rows of three parts side by side, part
+// q from column q * part_cols(E) on. Others: blocks of 32 tokens x 64 experts (what a product's shared
+// memory holds as one box), for each 32 tokens the blocks of the first 128 experts' three parts, then
+// the next 128's, so that g_router's kernel takes a block of tokens with one copy instead of six
+// (T = 16,383: 68 -> 65 us for both products). Columns past E hold zeros.
 __host__ __device__ constexpr int part_cols(int E) { return (E + 7) / 8 * 8; }
+__host__ __device__ constexpr bool side_by_side(int E) { return part_cols(E) <= 40; }
+__host__ __device__ constexpr int halves(int E) { return E > 64 ? 2 : 1; }  // blocks of 128 experts
+__host__ __device__ constexpr int blocks_of(int E) { return (E + 127) / 128 * 3 * halves(E); }
+// the block of part q, experts [64 kb, 64 kb + 64)
+__host__ __device__ constexpr int block_at(int E, int q, int kb) {
+  return (kb / halves(E) * 3 + q) * halves(E) + kb % halves(E);
+}
+__host__ __device__ constexpr int split_cols(int E) {  // columns that the split writes of a part
+  return side_by_side(E) ? part_cols(E) : (E + 127) / 128 * halves(E) * 64;
+}
+__host__ __device__ constexpr int64_t split_rows(int64_t T, int E) {
+  return side_by_side(E) ? T : (T + 31) / 32 * 32;
+}
+constexpr int64_t parts_size(int64_t T, int E) {
+  return split_rows(T, E) * (side_by_side(E) ? 3 * part_cols(E) : 64 * blocks_of(E));
+}
 // Expert rows of w's parts: whole steps of the contraction, zero past E.
 __host__ __device__ constexpr int w_rows(int E) { return (E + 15) / 16 * 16; }
 
@@ -41,28 +61,36 @@ __global__ void __launch_bounds__(256)
                              __nv_bfloat16* __restrict__ parts, const float* __restrict__ w, int H,
                              __nv_bfloat16* __restrict__ wparts) {
   dep_launch();
-  const int ec = part_cols(E) / 8, hc = H / 8;
+  const int ec = split_cols(E) / 8, hc = H / 8;
+  const int64_t rows = split_rows(T, E);
   int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   float v[8];
-  if (i < T * ec) {
+  if (i < rows * ec) {
     const int64_t t = i / ec;
     const int e = (int)(i - t * ec) * 8;
     const float* row = dl + t * ld + e;
-    if (vec && e + 8 <= E) {
+    if (vec && t < T && e + 8 <= E) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(row));
       const float4 b = __ldg(reinterpret_cast<const float4*>(row) + 1);
       v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
       v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = e + j < E ? __ldg(row + j) : 0.f;
+      for (int j = 0; j < 8; ++j) v[j] = t < T && e + j < E ? __ldg(row + j) : 0.f;
     }
-    uint4* to = reinterpret_cast<uint4*>(parts + t * 3 * part_cols(E) + e);
+    if (side_by_side(E)) {
+      uint4* to = reinterpret_cast<uint4*>(parts + t * 3 * part_cols(E) + e);
 #pragma unroll
-    for (int q = 0; q < 3; ++q) to[q * ec] = take_part(v);
+      for (int q = 0; q < 3; ++q) to[q * ec] = take_part(v);
+    } else {
+      uint4* to = reinterpret_cast<uint4*>(
+          parts + ((t / 32 * blocks_of(E) + block_at(E, 0, e / 64)) * 32 + t % 32) * 64 + e % 64);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) to[q * halves(E) * (32 * 64 / 8)] = take_part(v);
+    }
     return;
   }
-  i -= T * ec;
+  i -= rows * ec;
   if (!w || i >= (int64_t)w_rows(E) * hc) return;
   const int e = (int)(i / hc);
   const int64_t c = i - (int64_t)e * hc;
@@ -146,7 +174,7 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
   const int nkb = (int)((t1 - t0 + BK - 1) / BK);
   const int nbox = min(4, (p.H - h0) / 64);
   const int ep = STACK ? part_cols(p.E) : min(part_cols(p.E) - e0, 128);
-  const int na = (STACK ? 3 * ep : ep) > 64 ? 2 : 1;  // 64-expert boxes of a part
+  const int na = STACK ? (3 * ep > 64 ? 2 : 1) : halves(p.E);  // 64-expert boxes of a part
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NS; ++i) {
@@ -180,9 +208,11 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
         const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + C::A_BYTES, fb = full + 8 * s;
         const int t = (int)(t0 + (int64_t)kb * BK);
         mbar_expect_tx(fb, (C::PARTS * na + nbox) * BOX);
-        for (int q = 0; q < C::PARTS; ++q)
-          for (int i = 0; i < na; ++i)
-            tma_load_2d(a + (2 * q + i) * BOX, &tm_d, fb, q * part_cols(p.E) + e0 + 64 * i, t);
+        if constexpr (STACK) {
+          for (int i = 0; i < na; ++i) tma_load_2d(a + i * BOX, &tm_d, fb, 64 * i, t);
+        } else {
+          tma_load_4d(a, &tm_d, fb, 0, 0, blockIdx.y * 3 * na, t / BK);
+        }
         for (int i = 0; i < nbox; ++i) tma_load_2d(b + i * BOX, &tm_x, fb, h0 + 64 * i, t);
         ++issued;
       }
@@ -208,7 +238,7 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
         auto part = [&](uint32_t d, int q, bool fresh) {
 #pragma unroll
           for (int ks = 0; ks < BK / 16; ++ks)
-            umma_bf16(d, a + ((q * 2 * BOX + ks * 2048) >> 4), b + ((ks * 2048) >> 4), idesc,
+            umma_bf16(d, a + ((q * na * BOX + ks * 2048) >> 4), b + ((ks * 2048) >> 4), idesc,
                       fresh && ks == 0 ? 0u : 1u);
         };
         if constexpr (!STACK) {
@@ -494,8 +524,12 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
           if (!ok) break;
           const uint32_t a = smem_u32(sA + s * A_BYTES), fb = full + 8 * s;
           mbar_expect_tx(fb, A_BYTES + (RES ? 0 : nbox * 2 * KB * 128));
-          for (int q = 0; q < 2; ++q)
-            tma_load_2d(a + q * A_PART, &tm_d, fb, q * part_cols(p.E) + kb * KB, t * TM);
+          for (int q = 0; q < 2; ++q) {
+            if (side_by_side(p.E))
+              tma_load_2d(a + q * A_PART, &tm_d, fb, q * part_cols(p.E), t * TM);
+            else
+              tma_load_4d(a + q * A_PART, &tm_d, fb, 0, 0, block_at(p.E, q, kb), t * (TM / 32));
+          }
           if constexpr (!RES) {
             for (int q = 0; q < 2; ++q)
               for (int i = 0; i < nbox; ++i)
@@ -649,6 +683,16 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   }
 }
 
+// The parts in boxes of `tokens` x 64 experts side by side, else of `blocks` blocks by `tokens` / 32
+// blocks of 32 tokens.
+bool map_parts(CUtensorMap* m, const void* parts, int64_t T, int E, uint32_t blocks,
+               uint32_t tokens) {
+  if (side_by_side(E)) return map_bf16_2d(m, parts, 3 * part_cols(E), T, 64, tokens);
+  const uint64_t dims[4] = {64, 32, (uint64_t)blocks_of(E), (uint64_t)(split_rows(T, E) / 32)};
+  const uint32_t box[4] = {64, 32, blocks, tokens / 32};
+  return map_bf16(m, parts, 4, dims, box);
+}
+
 template <class K>
 bool grow_smem(OncePerDevice& once, K kernel, int bytes) {
   return once([&] {
@@ -689,19 +733,19 @@ int64_t stretch(int64_t T, int64_t E, int64_t H) {
 }  // namespace
 
 void router_grad_tc_layout(int64_t T, int64_t E, int64_t H, Carver& c, RouterGradWs& w) {
-  w.parts = c.take<uint16_t>(T * 3 * part_cols((int)E));
+  w.parts = c.take<uint16_t>(parts_size(T, (int)E));
   w.w_parts = c.take<uint16_t>(2 * w_rows((int)E) * H);
   const int64_t s = ceil_div(T, stretch(T, E, H));
   w.g_part = c.take<float>(s > 1 ? s * E * H : 1);
 }
 
 usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cudaStream_t st) {
-  const int E = (int)a.E, H = (int)a.H, ep = part_cols(E), ke = w_rows(E);
+  const int E = (int)a.E, H = (int)a.H, ke = w_rows(E);
   __nv_bfloat16* parts = static_cast<__nv_bfloat16*>(ws.parts);
   __nv_bfloat16* wparts = static_cast<__nv_bfloat16*>(ws.w_parts);
   {
     USAF_TRACE("router_grad_split", st);
-    const int64_t n = a.T * (ep / 8) + (a.dx ? (int64_t)ke * (H / 8) : 0);
+    const int64_t n = split_rows(a.T, E) * (split_cols(E) / 8) + (a.dx ? (int64_t)ke * (H / 8) : 0);
     const int vec = a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.dlogit) & 15) == 0;
     router_grad_split_kernel<<<(unsigned)ceil_div(n, 256), 256, 0, st>>>(
         a.dlogit, a.ld, a.T, E, vec, parts, a.dx ? a.w_router : nullptr, H, wparts);
@@ -710,7 +754,7 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
   const int64_t per = stretch(a.T, E, H), splits = ceil_div(a.T, per);
   if (a.g_router) {
     CUtensorMap d, x;
-    if (!map_bf16_2d(&d, parts, 3 * ep, a.T, 64, gw::BK) ||
+    if (!map_parts(&d, parts, a.T, E, 3 * halves(E), gw::BK) ||
         !map_bf16_2d(&x, a.x, H, a.T, 64, gw::BK))
       return USAF_ERR_CUDA;
     gw::Params p{};
@@ -724,7 +768,7 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
     p.status = a.status;
     const dim3 grid((unsigned)ceil_div(H, gw::N), (unsigned)ceil_div(E, 128), (unsigned)splits);
     // three parts fit the 128 rows of one A
-    USAF_TRY(ep <= 40 ? launch_w<true>(d, x, p, grid, st) : launch_w<false>(d, x, p, grid, st));
+    USAF_TRY(side_by_side(E) ? launch_w<true>(d, x, p, grid, st) : launch_w<false>(d, x, p, grid, st));
   }
   const bool sum = a.g_router && splits > 1;
   if (!a.dx) {
@@ -736,7 +780,7 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
   CUtensorMap d, w, in, out;
   const uint32_t wrows = ke <= gx::MAX_RES ? ke : gx::KB;
   const int64_t groups = ceil_div(H, gx::NH), tiles = ceil_div(a.T, gx::TM);
-  if (!map_bf16_2d(&d, parts, 3 * ep, a.T, 64, gx::TM) ||
+  if (!map_parts(&d, parts, a.T, E, 1, gx::TM) ||
       !map_bf16_2d(&w, wparts, H, 2 * ke, 64, wrows) ||
       !map_bf16_2d(&out, a.dx, H, a.T, 64, gx::TM) ||
       !map_bf16_2d(&in, a.dx_in ? a.dx_in : a.dx, H, a.T, 64, gx::TM))
