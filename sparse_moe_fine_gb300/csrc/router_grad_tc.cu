@@ -207,13 +207,13 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
         if (!ok) break;
         const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + C::A_BYTES, fb = full + 8 * s;
         const int t = (int)(t0 + (int64_t)kb * BK);
-        mbar_expect_tx(fb, (C::PARTS * na + nbox) * BOX);
+        mbar_expect_tx(fb, C::PARTS * na * BOX + B_BYTES);
         if constexpr (STACK) {
           for (int i = 0; i < na; ++i) tma_load_2d(a + i * BOX, &tm_d, fb, 64 * i, t);
         } else {
           tma_load_4d(a, &tm_d, fb, 0, 0, blockIdx.y * 3 * na, t / BK);
         }
-        for (int i = 0; i < nbox; ++i) tma_load_2d(b + i * BOX, &tm_x, fb, h0 + 64 * i, t);
+        tma_load_3d(b, &tm_x, fb, 0, t, h0 / 64);  // four boxes, zeros past the last feature
         ++issued;
       }
       if (!ok) *abort_flag = 1;
@@ -689,8 +689,9 @@ bool map_parts(CUtensorMap* m, const void* parts, int64_t T, int E, uint32_t blo
                uint32_t tokens) {
   if (side_by_side(E)) return map_bf16_2d(m, parts, 3 * part_cols(E), T, 64, tokens);
   const uint64_t dims[4] = {64, 32, (uint64_t)blocks_of(E), (uint64_t)(split_rows(T, E) / 32)};
+  const uint64_t pitch[3] = {128, 128 * 32, 128 * 32 * dims[2]};
   const uint32_t box[4] = {64, 32, blocks, tokens / 32};
-  return map_bf16(m, parts, 4, dims, box);
+  return map_bf16(m, parts, 4, dims, pitch, box);
 }
 
 template <class K>
@@ -754,8 +755,11 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
   const int64_t per = stretch(a.T, E, H), splits = ceil_div(a.T, per);
   if (a.g_router) {
     CUtensorMap d, x;
+    // x as (64 features, token, group of 64 features)
+    const uint64_t dims[3] = {64, (uint64_t)a.T, (uint64_t)H / 64}, pitch[2] = {(uint64_t)H * 2, 128};
+    const uint32_t box[3] = {64, gw::BK, gw::N / 64};
     if (!map_parts(&d, parts, a.T, E, 3 * halves(E), gw::BK) ||
-        !map_bf16_2d(&x, a.x, H, a.T, 64, gw::BK))
+        !map_bf16(&x, a.x, 3, dims, pitch, box))
       return USAF_ERR_CUDA;
     gw::Params p{};
     p.T = a.T;

@@ -75,6 +75,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int c0, int c1, int c2, int c3) {
   asm volatile(
@@ -200,9 +208,10 @@ __device__ __forceinline__ float trunc_rest(float a) {
   return a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u);
 }
 
-// A dense row-major bf16 array of `rank` axes, innermost first, in boxes, 128-byte swizzle. Host.
+// A bf16 array of `rank` axes, innermost first, in boxes, 128-byte swizzle; pitch[i]: bytes from one
+// entry of axis i + 1 to the next. Host.
 inline bool map_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                     const uint32_t* box) {
+                     const uint64_t* pitch, const uint32_t* box) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
     void* ptr = nullptr;
@@ -215,12 +224,10 @@ inline bool map_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t*
   }
   cuuint64_t d[4], strides[3];
   cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
-  uint64_t pitch = 2;
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     bx[i] = box[i];
-    pitch *= dims[i];
-    if (i + 1 < rank) strides[i] = pitch;
+    if (i + 1 < rank) strides[i] = pitch[i];
   }
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d,
             strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -228,9 +235,9 @@ inline bool map_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t*
 }
 inline bool map_bf16_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
                         uint32_t box_cols, uint32_t box_rows) {
-  const uint64_t dims[2] = {cols, rows};
+  const uint64_t dims[2] = {cols, rows}, pitch[1] = {cols * 2};
   const uint32_t box[2] = {box_cols, box_rows};
-  return map_bf16(m, base, 2, dims, box);
+  return map_bf16(m, base, 2, dims, pitch, box);
 }
 
 }  // namespace tcx
