@@ -224,18 +224,20 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {  // ------------------------------------------------ MMAs
+    {  // ------------------------------------------------------------ MMAs
+      const bool leader = elect_one();
       const uint32_t idesc = idesc_bf16(64 * nbox, true, true);
       const uint64_t ad0 = sdesc(smem_u32(smem), BOX, 1024);
       const uint64_t bd0 = sdesc(smem_u32(smem) + C::A_BYTES, BOX, 1024);
       bool ok = true;
       for (int kb = 0; kb < nkb; ++kb) {
         const int s = kb % C::NS;
-        ok = mbar_wait(full + 8 * s, (kb / C::NS) & 1, abort_flag);
+        ok = mbar_wait_all(full + 8 * s, (kb / C::NS) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         const uint64_t a = ad0 + ((s * C::STAGE) >> 4), b = bd0 + ((s * C::STAGE) >> 4);
         auto part = [&](uint32_t d, int q, bool fresh) {
+          if (!leader) return;
 #pragma unroll
           for (int ks = 0; ks < BK / 16; ++ks)
             umma_bf16(d, a + ((q * na * BOX + ks * 2048) >> 4), b + ((ks * 2048) >> 4), idesc,
@@ -249,17 +251,23 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
         const bool fresh = kb % FLUSH == 0;
         if (fresh) {  // the accumulator's last sums have been read
           const int use = STACK ? turn >> 1 : turn;  // how often it has been used before
-          ok = mbar_wait(given + 8 * acc, (use & 1) ^ 1, abort_flag);
+          ok = mbar_wait_all(given + 8 * acc, (use & 1) ^ 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
         }
         part(tmem + acc * N, 0, fresh);
-        umma_commit(empty + 8 * s);
-        if (kb % FLUSH == FLUSH - 1 || kb == nkb - 1) umma_commit(taken + 8 * acc);
+        if (leader) {
+          umma_commit(empty + 8 * s);
+          if (kb % FLUSH == FLUSH - 1 || kb == nkb - 1) umma_commit(taken + 8 * acc);
+        }
+        __syncwarp();
       }
       if (!ok) *abort_flag = 1;
-      umma_commit(done);
-      mbar_drain(done, 0, clock64() + TIMEOUT_CYCLES);
+      if (leader) {
+        umma_commit(done);
+        mbar_drain(done, 0, clock64() + TIMEOUT_CYCLES);
+      }
+      __syncwarp();
     }
   } else {  // ---------------------------------------------------- epilogue
     const int q = warp & 3, col = (warp - 2) >> 2;  // lanes' quarter, box of columns

@@ -60,6 +60,27 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
   }
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
+// The same by a whole warp, whose lanes stay together.
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity,
+                                              volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || clock64() - t0 > TIMEOUT_CYCLES)) return false;
+  }
+}
+// True in one lane of the (converged) warp, always the same. Roles that issue tensor-core work run
+// as whole warps and issue under this: their addresses and descriptors then stay in uniform
+// registers, where a role run by one lane has to move each of them there for every instruction
+// (about 100 cycles an MMA, more than a 128 x 128 x 16 MMA itself takes).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(is));
+  return is != 0;
+}
 // Wait for work this thread has already issued: it completes whatever the other roles do, so only
 // the deadline bounds it.
 __device__ __forceinline__ bool mbar_drain(uint32_t bar, uint32_t parity, long long deadline) {
