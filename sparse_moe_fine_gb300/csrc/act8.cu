@@ -7,6 +7,13 @@
 // instructions a value by two uses of fp32's exact integers: adding 1.5 * 2^23 leaves a rounded
 // (to nearest even) code in the low byte, and a code byte put into 2^23's mantissa is the code plus
 // a constant.
+//
+// Blocks of 16 with a power of two: on Gaussian values int8 codes are off by 0.73% in norm (0.47%
+// with an exact scale, whose codes and values would have to be rounded twice), 8-bit floats of three
+// mantissa bits by 2.6%. The exponent byte adds 1/16 to the store.
+// Measured (Qwen3-30B-A3B-shaped layer: T 4096, top 8, H 2048, I 768, bf16): save 34 us for 179 MB,
+// restore 74 us for 365 MB, of which 302 MB are written, and writes alone run at 4.0 TB/s on this
+// part (75 us). Mixtral-8x7B-shaped (T 8192, I 14336): both 582 us for 3.69 GB, 93% of the copy rate.
 #include "tc_ptx.cuh"
 #include "train.cuh"
 
@@ -163,6 +170,9 @@ __device__ __forceinline__ bool encode_block(const T* src, int n, int8_t* code, 
 
 constexpr int SAVE_U = 4;  // vectors of a lane in flight
 
+// A warp per run of a feature's rows, all blocks the machine holds at once: 34 us for 117 MB in and
+// 62 MB out on the Qwen3-shaped layer (issue slots 67% busy, DRAM 60%).
+
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
     act8_save_kernel(const Act8Args a, const T* __restrict__ x, const T* __restrict__ h,
@@ -241,8 +251,9 @@ __device__ __forceinline__ float silu_tail(float g) {
   }
 }
 
-// Rows [seg, seg + 32 vectors) of `nf` features from feature `f0` on, one warp a feature: h decoded,
-// wa formed again. The lanes' routing weights stay in registers over the features.
+// Rows [seg, seg + 32 vectors) of up to 64 features from feature `f0` on, one warp a feature: h
+// decoded, wa formed again. The lanes' routing weights stay in registers over the features. With x:
+// 43 us for 226 MB (Qwen3-shaped layer), 5.3 TB/s.
 constexpr int ROW_FEATURES = 64;  // features of a block: eight per warp
 template <typename T>
 __device__ __forceinline__ void restore_rows(const Act8Args& a, int64_t seg, int64_t f0, T* h,
@@ -348,7 +359,9 @@ __device__ __forceinline__ void restore_x(const Act8Args& a, int64_t blk, T* x) 
 // The eight lanes of a quarter-warp write eight row chunks of one feature, so every 16-byte store
 // into the 128-byte swizzled box is free of bank conflicts, and a row's four feature groups are one
 // 32-byte sector of codes. A block keeps its rows' tokens over G_STEPS feature tiles; the copy engine
-// reads a tile while the next one's codes are on their way. H a multiple of 64.
+// reads a tile while the next one's codes are on their way. H a multiple of 64. 38 us for 134 MiB
+// written (Qwen3-shaped layer), the time that clearing as much memory takes; wider and taller tiles
+// were no faster.
 constexpr int G_ROWS = 256, G_FEATURES = 64, G_STEPS = 4;
 constexpr int G_SMEM = 4 * 8192 + 1024;
 __device__ __forceinline__ void gather_bf16(const CUtensorMap& tm, const Act8Args& a, int rb,
