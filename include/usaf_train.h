@@ -85,8 +85,9 @@ usaf_status usaf_router_aux_bwd(int64_t T, int64_t E, int64_t k, const float* lo
  *   x         needed for g_router;  w_router [E,H] fp32, needed for dx
  *   g_in      [E,H] fp32 or NULL (zero);  g_router [E,H] fp32 out, or NULL to skip; may be g_in
  *   dx_in     [T,H] or NULL (zero);  dx [T,H] out, or NULL to skip; may be dx_in
- *   dev_status gets USAF_DEV_NONFINITE if a produced gradient is NaN/Inf, USAF_DEV_TIMEOUT if a
- *              tensor-core kernel gave up a wait
+ *             Neither output may overlap any other input (dx = x is refused).
+ *   dev_status gets USAF_DEV_NONFINITE if a produced gradient is NaN/Inf (of bf16 layers an infinite
+ *              dlogit or w_router gives NaN), USAF_DEV_TIMEOUT if a tensor-core kernel gave up a wait
  * Sums are fp32 with dlogit carried exactly into g_router (three bf16 parts) and to 2^-16 into dx
  * of bf16 layers; their order is fixed. The workspace and, of bf16 layers, x, dx_in, dx and
  * w_router must be 16-byte aligned (INVALID_ARG otherwise).

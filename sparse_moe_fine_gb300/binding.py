@@ -581,6 +581,17 @@ def _on(stream, dev):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _ws_on(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace of the stream that the call runs on: the allocator may hand its memory out again as
+    soon as the call returns, and then only behind the call's work."""
+    if stream is None:
+        return _ws(nbytes, device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream, device)
+    with torch.cuda.stream(stream):
+        return _ws(nbytes, device)
+
+
 def router_aux_workspace_size(T: int, E: int, k: int, G: int = 1) -> int:
     return int(lib().usaf_router_aux_workspace_size(int(T), int(E), int(k), int(G)))
 
@@ -598,12 +609,12 @@ def router_aux_fwd(logits, topk_idx, k, count, prob_sum, n_tok, loss, coef_balan
     if group_offset is None and G != 1:
         raise ValueError("group_offset is required")
     if ws is None:
-        ws = _ws(router_aux_workspace_size(T, E, k, G), logits.device)
+        ws = _ws_on(router_aux_workspace_size(T, E, k, G), logits.device, stream)
     _check("usaf_router_aux_fwd", lib().usaf_router_aux_fwd(
-        T, E, k, lp, ld, _ok("topk_idx", topk_idx, _i32, (T * k,), d),
+        T, E, int(k), lp, ld, _ok("topk_idx", topk_idx, _i32, (T * k,), d),
         _opt("token_mask", token_mask, _u8, (T,), d),
-        _opt("group_offset", group_offset, _i32, (G + 1,), d), G, coef_balance, coef_z,
-        _ok("count", count, _i32, ge, d), _ok("prob_sum", prob_sum, _f32, ge, d),
+        _opt("group_offset", group_offset, _i32, (G + 1,), d), G, float(coef_balance),
+        float(coef_z), _ok("count", count, _i32, ge, d), _ok("prob_sum", prob_sum, _f32, ge, d),
         _ok("n_tok", n_tok, _i32, (G,), d), _ok("loss", loss, _f32, (3,), d), _ptr(dev_status),
         ws.data_ptr(), ws.numel(), _on(stream, d)))
 
@@ -620,9 +631,9 @@ def router_aux_bwd(logits, k, count, n_tok, dlogit, coef_balance, coef_z, d_loss
     if group_offset is None and G != 1:
         raise ValueError("group_offset is required")
     _check("usaf_router_aux_bwd", lib().usaf_router_aux_bwd(
-        T, E, k, lp, ld, _opt("token_mask", token_mask, _u8, (T,), d),
-        _opt("group_offset", group_offset, _i32, (G + 1,), d), G, coef_balance, coef_z,
-        _ok("count", count, _i32, (G, E), d), _ok("n_tok", n_tok, _i32, (G,), d),
+        T, E, int(k), lp, ld, _opt("token_mask", token_mask, _u8, (T,), d),
+        _opt("group_offset", group_offset, _i32, (G + 1,), d), G, float(coef_balance),
+        float(coef_z), _ok("count", count, _i32, (G, E), d), _ok("n_tok", n_tok, _i32, (G,), d),
         _opt("d_loss", d_loss, _f32, (1,), d), op, ldo, int(accumulate), _ptr(dev_status),
         _on(stream, d)))
 
@@ -645,7 +656,7 @@ def router_grad(dlogit, x, w_router, g_router=None, g_in=None, dx=None, dx_in=No
     dp, ld = _ok_rows("dlogit", dlogit, _f32, (T, E), d)
     th, eh = (T, H), (E, H)
     if ws is None:
-        ws = _ws(router_grad_workspace_size(T, E, H, dt), dlogit.device)
+        ws = _ws_on(router_grad_workspace_size(T, E, H, dt), dlogit.device, stream)
     _check("usaf_router_grad", lib().usaf_router_grad(
         T, E, H, _dt(ref), dp, ld, _opt("x", x, dt, th, d),
         _opt("w_router", w_router, _f32, eh, d), _opt("g_in", g_in, _f32, eh, d),

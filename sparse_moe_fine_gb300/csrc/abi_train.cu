@@ -124,6 +124,8 @@ usaf_status usaf_router_grad(int64_t T, int64_t E, int64_t H, usaf_dtype dtype,
                              size_t ws_bytes, void* stream) {
   if (!grad_shape_ok(T, E, H, dtype) || !dlogit || ld_dlogit < E) return USAF_ERR_INVALID_ARG;
   if ((!g_router && !dx) || (g_router && !x) || (dx && !w_router)) return USAF_ERR_INVALID_ARG;
+  // dx is written while g_router's product may still read x
+  if (g_router && dx && dx == x) return USAF_ERR_INVALID_ARG;
   if (dtype == USAF_BF16) {
     if (H % 64 != 0) return USAF_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(dx_in) || !aligned16(dx) || !aligned16(w_router))

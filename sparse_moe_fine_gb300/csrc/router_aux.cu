@@ -26,7 +26,7 @@ constexpr int FIN_THREADS = 32 * FIN_WARPS;
 // Rows that a lane has in flight: 16 values at most.
 template <int NV>
 constexpr int ROWS = NV <= 4 ? 4 : (NV <= 8 ? 2 : 1);
-constexpr int MAX_CHUNK = 8192;  // a token's flag is a byte of shared memory
+constexpr int MAX_CHUNK = 4096;  // a token's flag is a byte of shared memory
 // Blocks of an SM: four (64 registers a thread) hold the chunks of 16,383 tokens in one wave, where
 // the compiler's own choice needs two (28.7 -> 26.7 us); 32 values a lane need the registers.
 template <int NV>
@@ -703,8 +703,9 @@ void aux_ws_layout(int64_t T, int64_t E, int64_t G, Carver& c, AuxWs& w) {
 usaf_status aux_fwd_launch(const AuxArgs& a, int32_t* count, float* prob_sum, int32_t* n_tok,
                            float* loss, const AuxWs& w, cudaStream_t st) {
   const AuxParams p = make_params(a);
-  const size_t smem = (size_t)(AUX_WARPS + 1) * a.E * 4 + p.chunk;  // at most 45 KB
-  const bool one = p.nchunks == 1;
+  const size_t smem = (size_t)(AUX_WARPS + 1) * a.E * 4 + p.chunk;  // at most 40 KB
+  // one block for everything, while it also clears the outputs of every group in little time
+  const bool one = p.nchunks == 1 && a.G * a.E <= (1 << 16);
   USAF_TRY(by_width(a.E, rows_vec(a.logits, a.ld, a.E), [&](auto lpr, auto nv, auto vec) {
     USAF_TRACE("router_aux_part", st);
     auto go = [&](auto kernel) {

@@ -30,9 +30,12 @@ usaf_status launch_dep(void (*kernel)(P...), dim3 grid, unsigned threads, size_t
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+    cudaGetLastError();  // reported here, not again by the next launch's check
+    return USAF_ERR_CUDA;
+  }
   count_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? USAF_OK
-                                                                                  : USAF_ERR_CUDA;
+  return USAF_OK;
 }
 
 // Runs set() once for each device that is current when it is called (a kernel's attributes belong to

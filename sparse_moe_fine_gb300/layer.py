@@ -162,7 +162,8 @@ class MoELayer:
         """The sequences that the auxiliary losses see in the next batches: group_offset [G+1] int32
         (first token of each packed sequence; None: the batch is one) and token_mask [T] uint8 (0:
         a padding token that takes no part; None: every token does). The tensors are read by every
-        later step, so a caller that changes only their contents may write into them. With the
+        later step, so a caller that changes only their contents may write into them; they are not
+        part of a checkpoint. With the
         losses on: aux_count and aux_prob [G,E], aux_n [G] and aux_loss [3] (total, balance, z) hold
         the last forward's values."""
         if not self.aux:
@@ -229,9 +230,9 @@ class MoELayer:
     def share_activations(self, other):
         """Use another layer's x_perm, h and wa (of the same shape): for layers whose activations
         are kept by save_act8 between their forward and their backward."""
-        if (self.dtype, self.x_perm.shape, self.h.shape) != (other.dtype, other.x_perm.shape,
-                                                             other.h.shape):
-            raise ValueError("layers of different shapes cannot share activation buffers")
+        mine, theirs = ((L.dtype, L.h.device, L.x_perm.shape, L.h.shape) for L in (self, other))
+        if mine != theirs:
+            raise ValueError("layers of different shapes or devices cannot share activation buffers")
         self.x_perm, self.h, self.wa = other.x_perm, other.h, other.wa
         self._graphs = {}  # captured steps hold the old buffers' pointers
 

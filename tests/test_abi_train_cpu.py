@@ -72,13 +72,13 @@ def test_aux_refusals():
 def test_router_grad_refusals():
     L = B.lib()
 
-    def call(T=8, E=4, H=64, dt=1, dl=FAKE, ld=4, x=FAKE, w=FAKE, g=FAKE, dx=FAKE, ws=FAKE,
-             n=1 << 30):
+    def call(T=8, E=4, H=64, dt=1, dl=FAKE, ld=4, x=FAKE, w=FAKE, g=FAKE,
+             dx=ctypes.c_void_p(1 << 20), ws=FAKE, n=1 << 30):
         return L.usaf_router_grad(T, E, H, dt, dl, ld, x, w, None, g, None, dx, None, ws, n, None)
 
     for bad in (dict(T=0), dict(E=0), dict(H=0), dict(dt=2), dict(dl=None), dict(ld=3),
                 dict(g=None, dx=None), dict(x=None), dict(w=None), dict(x=ctypes.c_void_p(4104)),
-                dict(dx=ctypes.c_void_p(4098))):
+                dict(dx=ctypes.c_void_p(4098)), dict(x=FAKE, dx=FAKE)):
         assert call(**bad) == 1, bad
     assert call(H=96) == 2           # bf16 needs a multiple of 64
     assert call(ws=None) == 3 and call(n=0) == 3

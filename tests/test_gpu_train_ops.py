@@ -92,7 +92,7 @@ def _aux_check(got, ref, base=None):
     (1, 1, 1, 1), (1, 8, 2, 1), (3, 5, 5, 1), (128, 8, 2, 1), (31, 16, 3, 2), (65, 24, 4, 9),
     (300, 60, 4, 5), (257, 128, 8, 3), (1000, 129, 8, 1), (511, 256, 6, 7), (70, 500, 3, 4),
     (65, 1024, 32, 2), (4096, 128, 8, 1), (4099, 8, 2, 64), (9731, 128, 8, 37), (200, 16, 4, 200),
-    (24, 9, 6, 13), (2000, 128, 8, 1500), (135, 300, 8, 51),
+    (24, 9, 6, 13), (2000, 128, 8, 1500), (135, 300, 8, 51), (20, 1024, 4, 90),
     (20011, 96, 6, 3)])
 @pytest.mark.parametrize("mask", ["none", "some", "all"])
 def test_aux_matches_fp64(T, E, k, G, mask):
