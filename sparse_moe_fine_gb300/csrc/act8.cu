@@ -434,28 +434,41 @@ __device__ __forceinline__ void gather_bf16(const CUtensorMap& tm, const Act8Arg
   if (threadIdx.x == 0) tcx::bulk_wait();
 }
 
-// The same for fp32 tokens and for widths that are no multiple of 64.
+// The same for fp32 tokens and for widths that are no multiple of 64: 128 rows x 64 features through
+// shared memory. Each code's address waits on its row's token and each thread has only bytes to load, so
+// latency bounds it: the tokens are read once per tile and eight values of a thread are on their way at
+// a time (restore of 4,096 fp32 tokens, 128 experts, top 8, H 2,048: 242 us with one at a time, 176 us so).
 constexpr int XG_ROWS = 128;
 template <typename T>
 __global__ void __launch_bounds__(THREADS) act8_gather_kernel(const Act8Args a, T* x_perm) {
   __shared__ T tile[64][XG_ROWS + 1];
+  __shared__ int s_tok[XG_ROWS];  // the rows' tokens, -1 without one
   const int64_t r0 = (int64_t)blockIdx.x * XG_ROWS;
   const int64_t h0 = (int64_t)blockIdx.y * 64;
   const int64_t end = a.rt.expert_offset[a.s.E], nbx = (a.s.H + BLK - 1) / BLK;
-  for (int v = threadIdx.x; v < XG_ROWS * 64; v += THREADS) {
-    const int r = v / 64, f = v % 64;
-    const int64_t row = r0 + r, c = h0 + f;
-    float val = 0.f;
-    if (row < end && c < a.s.H && a.rt.perm_slot[row] >= 0) {
-      const int64_t t = a.rt.perm_tok[row];
-      val = (float)a.x_code[t * a.s.H + c] * value_factor(a.x_exp[t * nbx + c / BLK]);
+  for (int r = threadIdx.x; r < XG_ROWS; r += THREADS)
+    s_tok[r] = r0 + r < end && a.rt.perm_slot[r0 + r] >= 0 ? a.rt.perm_tok[r0 + r] : -1;
+  __syncthreads();
+  constexpr int U = 8;
+  const int f = threadIdx.x % 64;
+  const int64_t c = h0 + f;
+  for (int r1 = threadIdx.x / 64; r1 < XG_ROWS; r1 += U * (THREADS / 64)) {
+    int code[U], e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = s_tok[r1 + u * (THREADS / 64)];
+      const bool live = t >= 0 && c < a.s.H;
+      code[u] = live ? __ldg(a.x_code + t * a.s.H + c) : 0;
+      e[u] = live ? __ldg(a.x_exp + t * nbx + c / BLK) : 0;
     }
-    tile[f][r] = from_f32<T>(val);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      tile[f][r1 + u * (THREADS / 64)] = from_f32<T>((float)code[u] * value_factor(e[u]));
   }
   __syncthreads();
   for (int v = threadIdx.x; v < XG_ROWS * 64; v += THREADS) {
-    const int f = v / XG_ROWS, r = v % XG_ROWS;
-    if (h0 + f < a.s.H) x_perm[(h0 + f) * a.R_cap + r0 + r] = tile[f][r];
+    const int fo = v / XG_ROWS, r = v % XG_ROWS;
+    if (h0 + fo < a.s.H) x_perm[(h0 + fo) * a.R_cap + r0 + r] = tile[fo][r];
   }
 }
 
