@@ -417,10 +417,10 @@ __global__ void __launch_bounds__(FIN_THREADS)
   const int g = blockIdx.x / nb, eb = blockIdx.x % nb, e = eb * el + tx;
   float a = 0.f, z = 0.f;
   int32_t c = 0, n = 0;
-  const int64_t o0 = clamp_off(p, g), o1 = clamp_off(p, g + 1);
-  const int64_t ch0 = o0 / p.chunk, ch1 = o1 > o0 ? (o1 - 1) / p.chunk : ch0 - 1;
   dep_launch();
   dep_wait();
+  const int64_t o0 = clamp_off(p, g), o1 = clamp_off(p, g + 1);
+  const int64_t ch0 = o0 / p.chunk, ch1 = o1 > o0 ? (o1 - 1) / p.chunk : ch0 - 1;
   if (e < p.E) {
     const float* pp = w.prob + (ch0 + ls + g) * p.E + e;
     const int32_t* pc = w.count + (ch0 + ls + g) * p.E + e;

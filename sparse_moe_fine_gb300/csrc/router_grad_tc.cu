@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(gw::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   dep_wait();    // the parts are written
-  dep_launch();  // dx's kernel may start: it reads the parts, and waits before it reads the sums
+  dep_launch();  // dx's kernel may be set up beside this one
 
   if (warp == 0) {
     if (lane == 0) {  // ------------------------------------------------ loads
@@ -527,7 +527,9 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (!p.sum) dep_wait();  // else the kernel before is g_router's, which saw the parts written
+  // Every thread waits, the loading ones too: that g_router's kernel has seen the parts written orders
+  // nothing for this grid, only that kernel's end does.
+  dep_wait();
   float odd = 0.f;  // NaN once a produced value was not finite
 
   if (warp == 0) {
@@ -636,7 +638,6 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
     const bool issuer = ((warp - 3) & 3) == 0 && lane == 0;
     const int row = q * 32 + lane;
     if (p.sum) {
-      dep_wait();  // every stretch's sums are there
       constexpr int N = 32 * EPI_WARPS;
       reduce_parts(p.sum, p.splits, (int64_t)p.E * p.H, p.g_in, p.g_router, p.status,
                    (int64_t)blockIdx.x * N + threadIdx.x - 96, (int64_t)gridDim.x * N);

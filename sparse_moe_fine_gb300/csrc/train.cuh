@@ -9,8 +9,9 @@
 namespace usaf {
 
 // A kernel that may be set up while the one before it in the stream still runs: it must pass
-// dep_wait() before it touches memory that other kernels write or read. A kernel lets the next one
-// in by dep_launch(); one that never does lets it in when it ends.
+// dep_wait(), in every thread, before it touches memory that other kernels write or read, whichever
+// of the kernels before it that was: a kernel that has let the next one in orders nothing for it before
+// it ends. A kernel lets the next one in by dep_launch(); one that never does lets it in when it ends.
 __device__ __forceinline__ void dep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -1,0 +1,50 @@
+"""Launch paths of the calls of include/usaf_train.h that take larger sizes, their order among one
+another, and their behaviour in the layer and the stack.
+
+Bounds are those of the fp32 arithmetic, u = 2^-24: see each test. Restatements in fp64 are
+oracle/train_oracle.py's.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import train_oracle as TO
+from sparse_moe_fine_gb300 import binding as B
+
+from _gpu import device, rel_l2, to_dev
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,E,H", [(4096, 128, 2048), (1500, 8, 512), (900, 300, 256)])
+def test_router_grad_calls_in_a_row_on_one_workspace(T, E, H):
+    """Calls that follow one another at once, on other inputs and one workspace, give the bits that
+    each gives alone: no kernel of a call reads parts or sums before they are written."""
+    dev = device()
+    g = torch.Generator(device=dev)
+    g.manual_seed(T)
+    rand = lambda *s: torch.randn(*s, generator=g, device=dev)
+    n = 4
+    dl, w = [rand(T, E) * 10.0 ** i for i in range(n)], [rand(E, H) for _ in range(n)]
+    x, xi = ([rand(T, H).bfloat16() for _ in range(n)] for _ in range(2))
+    ws = torch.empty(B.router_grad_workspace_size(T, E, H, torch.bfloat16), dtype=torch.uint8,
+                     device=dev)
+
+    def call(i):
+        gr, dx = torch.empty(E, H, device=dev), torch.empty_like(x[i])
+        B.router_grad(dl[i], x[i], w[i], g_router=gr, dx=dx, dx_in=xi[i], ws=ws)
+        return gr, dx
+
+    alone = []
+    for i in range(n):
+        torch.cuda.synchronize()
+        ws.fill_(255)  # NaN, so that a read of what is not yet written shows
+        torch.cuda.synchronize()
+        alone.append(call(i))
+        torch.cuda.synchronize()
+    for _ in range(5):
+        row = [call(i) for i in range(n)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, row):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert torch.isfinite(alone[0][0]).all() and torch.isfinite(alone[0][1].float()).all()
