@@ -88,9 +88,10 @@ usaf_status usaf_router_aux_bwd(int64_t T, int64_t E, int64_t k, const float* lo
  *             Neither output may overlap any other input (dx = x is refused).
  *   dev_status gets USAF_DEV_NONFINITE if a produced gradient is NaN/Inf (of bf16 layers an infinite
  *              dlogit or w_router gives NaN), USAF_DEV_TIMEOUT if a tensor-core kernel gave up a wait
- * Sums are fp32 with dlogit carried exactly into g_router (three bf16 parts) and to 2^-16 into dx
- * of bf16 layers; their order is fixed. The workspace and, of bf16 layers, x, dx_in, dx and
- * w_router must be 16-byte aligned (INVALID_ARG otherwise).
+ * Sums are fp32, their order is fixed. On tensor cores dlogit and w_router are carried exactly, as
+ * three bf16 parts each; of dx's products of two parts those below 2^-24 of the whole are left out.
+ * The workspace and, of bf16 layers, x, dx_in, dx and w_router must be 16-byte aligned (INVALID_ARG
+ * otherwise).
  * Limits: T >= 1, 1 <= E <= 1024, H >= 1, T < 2^31 - 65536, E*H < 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED (bf16 with H % 64 != 0; fp32 beyond 2^31 tiles of 64 x 64),
  * WORKSPACE, CUDA.

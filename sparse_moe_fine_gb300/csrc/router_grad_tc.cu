@@ -5,20 +5,19 @@
 //
 // dlogit and w are fp32; the tensor cores take bf16. Cutting a float to its upper 16 bits and doing
 // the same with what is left gives three bf16 numbers whose sum is exactly the float (8 bits each of
-// its 24), and a product of two bf16 numbers is exact in fp32. g_router, an fp32 result, uses all
-// three parts of dlogit (x is bf16 already). dx is rounded to bf16 at the end, so two parts of
-// dlogit and of w (2^-16 each) and three of their four products are enough. A first kernel writes
-// the parts (6 bytes a logit, which stay in L2); the products' kernels are then fed by TMA alone.
-// (Converting in the products' own kernels cost more: every feature group's CTA converts again.)
+// its 24), and a product of two bf16 numbers is exact in fp32. g_router uses all three parts of dlogit
+// (x is bf16 already). dx uses all three parts of both operands and the six of their nine products that
+// reach 2^-24 of the whole: a softmax's gradient sums to zero over the experts, so what the rows of w
+// have in common cancels, and an error relative to w itself does not. (With two parts and three
+// products, 2^-16, rows that differ by a thousandth of what they share gave 1% of error in dx, with
+// six 3e-5, fp32 arithmetic 1e-4.) A first kernel writes the parts (6 bytes a logit, which stay in L2);
+// the products' kernels are then fed by TMA alone. (Converting in the products' own kernels cost more:
+// every feature group's CTA converts again.)
 //
-// Measured, both products with dx_in: T 4096, E 128, H 2048 28 us (54 MB; 8 us at the copy rate);
-// T 8192, E 8, H 4096 46 us (202 MB; 30 us); T 16,383, E 128, H 2048 63 us (212 MB, 31 us; the bf16
-// products alone are 27 us of tensor time). What bounds them is at each kernel.
-// (Converting in the products' own kernels cost more: every feature group's CTA converts again.)
-//
-// Measured, both products with dx_in: T 4096, E 128, H 2048 28 us (54 MB; 8 us at the copy rate);
-// T 8192, E 8, H 4096 46 us (202 MB; 30 us); T 16,383, E 128, H 2048 63 us (212 MB, 31 us; the bf16
-// products alone are 27 us of tensor time). What bounds them is at each kernel.
+// Measured, both products with dx_in: T 4096, E 128, H 2048 31 us (54 MB; 8 us at the copy rate);
+// T 8192, E 8, H 4096 46 us (202 MB; 30 us); T 16,383, E 128, H 2048 73 us (212 MB, 31 us; the bf16
+// products alone are 40 us of tensor time). With dx's three products of two parts they were 29, 49 and
+// 64 us. What bounds them is at each kernel.
 #include "tc_ptx.cuh"
 #include "train.cuh"
 
@@ -50,8 +49,13 @@ __host__ __device__ constexpr int64_t split_rows(int64_t T, int E) {
 constexpr int64_t parts_size(int64_t T, int E) {
   return split_rows(T, E) * (side_by_side(E) ? 3 * part_cols(E) : 64 * blocks_of(E));
 }
-// Expert rows of w's parts: whole steps of the contraction, zero past E.
-__host__ __device__ constexpr int w_rows(int E) { return (E + 15) / 16 * 16; }
+// dx of at most 16 experts: the three parts' columns, side by side, are one axis of the contraction (a
+// box of 64 columns holds them), and w's rows are repeated for each part.
+__host__ __device__ constexpr bool stacked(int E) { return 3 * part_cols(E) <= 64; }
+// Rows of w's parts: whole steps of the contraction, zero past the experts.
+__host__ __device__ constexpr int w_rows(int E) {
+  return ((stacked(E) ? 3 * part_cols(E) : E) + 15) / 16 * 16;
+}
 
 // ------------------------------------------------------------------------------ parts
 __device__ __forceinline__ uint4 take_part(float (&v)[8]) {
@@ -102,8 +106,9 @@ __global__ void __launch_bounds__(256)
   }
   i -= rows * ec;
   if (!w || i >= (int64_t)w_rows(E) * hc) return;
-  const int e = (int)(i / hc);
-  const int64_t c = i - (int64_t)e * hc;
+  const int row = (int)(i / hc);
+  const int64_t c = i - (int64_t)row * hc;
+  const int e = stacked(E) ? (row < 3 * part_cols(E) ? row % part_cols(E) : E) : row;
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.f;
   if (e < E) {
@@ -112,11 +117,9 @@ __global__ void __launch_bounds__(256)
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
-  uint4* to = reinterpret_cast<uint4*>(wparts);
-  to[i] = take_part(v);
-  to[(int64_t)w_rows(E) * hc + i] =
-      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                 pack_bf16x2(v[6], v[7]));
+  uint4* to = reinterpret_cast<uint4*>(wparts) + i;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) to[q * (int64_t)w_rows(E) * hc] = take_part(v);
 }
 
 // ------------------------------------------------------------------------------ g_router
@@ -415,47 +418,53 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------------------ dx
-// A CTA owns 128 features and walks token tiles of 128: A = dlogit's two leading parts (K-major, 64
-// experts a block) through a ring, B = w's two parts, accumulators in tensor memory, twice. RES: B
-// for all experts stays in shared memory (at most 256 experts); else it comes through the ring with
-// A. dx_in comes and dx goes by TMA through a ring of 128 x 64 boxes in which the epilogue adds, so
-// token rows are read and written in whole lines while later tiles are on their way.
+// A CTA owns 128 features and walks token tiles of 128: A = dlogit's three parts (K-major, 64 experts
+// a block), B = w's three parts, accumulators in tensor memory, twice. A block's parts come one by one
+// through a ring of 16 KB slots, the leading one first, and each slot is free again after the products
+// that use it: three, two and one. RES: B for all experts stays in shared memory (at most 160 experts);
+// else its blocks come through the ring ahead of A's. STACK (RES, at most 16 experts): all parts of a
+// tile are one slot, whose products are w's three parts (T 8192, E 8, H 4096: both products 57 us with
+// three mostly empty slots a tile). dx_in comes and dx goes by TMA through a ring of
+// 128 x 64 boxes in which the epilogue adds, so token rows are read and written in whole lines while
+// later tiles are on their way. The shared memory that B leaves goes to boxes first (eight, four or
+// two), then to the ring.
 // The same launch adds up g_router's stretches (`sum`): its epilogue warps do so while the first
 // tiles are on their way, which saves a launch and hides most of the sum.
-// T 4096, E 128, H 2048: 16 us, of which 3 us until the first tile's parts are there, 2 us a tile.
-// T 16,383: 34 us for 134 MB of dx_in and dx, 4.1 TB/s; without any MMA or parts loaded it takes as
-// long, with eight boxes instead of four (few experts) 24 us. More boxes, blocks in flight or warps,
-// L2 prefetches and clusters that share the loads of the parts each bought nothing here.
+// T 16,383, E 128, H 2048: each of the 16 feature groups reads dlogit's parts, 201 MB between L2 and the
+// SMs beside 134 MB of dx_in and dx, with 64 KB of parts and 64 KB of boxes in flight on an SM; that
+// bounds it (two parts instead of three: 10 us less).
 namespace gx {
 constexpr int TM = 128;      // tokens of a tile
 constexpr int NH = 128;      // features of a CTA
-constexpr int KB = 64;       // experts of an A block
-constexpr int A_PART = TM * KB * 2;
-constexpr int A_BYTES = 2 * A_PART;
-constexpr int B_BLOCK = 2 * 2 * KB * 128;  // w's two parts, two groups of 64 features, KB experts
+constexpr int KB = 64;       // experts of a block
+constexpr int SLOT = TM * KB * 2;  // a part of A (128 tokens x 64 experts) or B (64 x 128 features)
 constexpr int BOX = TM * 64 * 2;
-constexpr int MAX_RES = 256;
-constexpr int MAX_NA = 3;
+constexpr int MAX_RES = 160;
+constexpr int MAX_RING = 10;
 constexpr int MAX_SLOTS = 8;
 constexpr int EPI_WARPS = 16;  // two boxes of a tile by two tiles by four quarters of lanes
 constexpr int THREADS = 96 + 32 * EPI_WARPS;
 constexpr int SMEM_MAX = 232448;
-// A blocks in the ring
-__host__ __device__ constexpr int ring(int ke) { return ke > 64 && ke <= 128 ? 3 : 2; }
-__host__ __device__ constexpr int b_bytes(int ke) {  // of the resident parts, or of the ring's blocks
-  return ke <= MAX_RES ? 2 * 2 * ke * 128 : ring(ke) * B_BLOCK;
+constexpr int EXTRA = 1024 + 512;  // alignment, barriers
+__host__ __device__ constexpr int b_bytes(int ke) {  // of the resident parts
+  return ke <= MAX_RES ? 3 * 2 * ke * 128 : 0;
+}
+__host__ __device__ constexpr int fit(int ke, int boxes) {  // ring slots beside that many boxes
+  return (SMEM_MAX - EXTRA - b_bytes(ke) - boxes * BOX) / SLOT;
 }
 // Boxes of the staging ring. A wait by parity tells a phase only from its neighbours, so a box's
 // barriers serve one epilogue group, whose tiles use the box in turn: with two groups a box (tiles
 // of either parity) that takes a multiple of four; where fewer fit, one group does all tiles.
 __host__ __device__ constexpr int slots(int ke) {
-  const int s = (SMEM_MAX - 1024 - 512 - ring(ke) * A_BYTES - b_bytes(ke)) / BOX;
-  return s >= MAX_SLOTS ? MAX_SLOTS : (s >= 4 ? 4 : 2);
+  if (ke > MAX_RES) return 4;
+  return fit(ke, 8) >= 3 ? 8 : (fit(ke, 4) >= 4 ? 4 : 2);
 }
-static_assert(slots(64) == 8 && slots(128) == 4, "two tiles at least");
-static_assert(2 * BOX + ring(MAX_RES) * A_BYTES + b_bytes(MAX_RES) + 1536 <= SMEM_MAX &&
-                  4 * BOX + ring(1024) * A_BYTES + b_bytes(1024) + 1536 <= SMEM_MAX,
-              "one tile at least");
+__host__ __device__ constexpr int ring(int ke) {
+  return fit(ke, slots(ke)) < MAX_RING ? fit(ke, slots(ke)) : MAX_RING;
+}
+static_assert(slots(64) == 8 && slots(128) == 4 && slots(MAX_RES) == 2, "boxes");
+// streamed B: a block's six parts and more
+static_assert(ring(64) >= 3 && ring(128) >= 4 && ring(MAX_RES) >= 4 && ring(1024) >= 7, "ring");
 struct Params {
   int64_t T;
   int E, H, ke;
@@ -470,7 +479,7 @@ struct Params {
 };
 }  // namespace gx
 
-template <bool RES>
+template <bool RES, bool STACK>
 __global__ void __launch_bounds__(gx::THREADS, 1)
     router_grad_x_tc_kernel(const __grid_constant__ CUtensorMap tm_d,
                             const __grid_constant__ CUtensorMap tm_w,
@@ -480,17 +489,19 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
+  static_assert(RES || !STACK, "stacked parts of few experts are resident");
+  constexpr int PARTS = STACK ? 1 : 3;  // slots of a block of A
   const int ke = p.ke, NS = p.slots, NA = p.ring;
-  uint8_t* sA = smem;
-  uint8_t* sStage = smem + NA * A_BYTES;
-  uint8_t* sB = sStage + NS * BOX;  // [part][feature group of 64][expert][64 features] (a block)
+  uint8_t* sRing = smem;
+  uint8_t* sStage = smem + NA * SLOT;
+  uint8_t* sB = sStage + NS * BOX;  // RES: [part][feature group of 64][expert][64 features]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sB + b_bytes(ke));
-  // full[], empty[] of the A ring, tfull[2], tempty[2], loaded[], added[], freed[] of the boxes, done,
+  // full[], empty[] of the ring, tfull[2], tempty[2], loaded[], added[], freed[] of the boxes, done,
   // wfull
-  const uint32_t full = smem_u32(bars), empty = full + 8 * MAX_NA, tfull = empty + 8 * MAX_NA,
+  const uint32_t full = smem_u32(bars), empty = full + 8 * MAX_RING, tfull = empty + 8 * MAX_RING,
                  tempty = tfull + 16, loaded = tempty + 16, added = loaded + 8 * MAX_SLOTS,
                  freed = added + 8 * MAX_SLOTS, done = freed + 8 * MAX_SLOTS, wfull = done + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_NA + 4 + 3 * MAX_SLOTS + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_RING + 4 + 3 * MAX_SLOTS + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr uint32_t COLS = 2 * NH;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -500,8 +511,7 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   const int tiles = (int)((p.T + TM - 1) / TM);
   const int nbox = min(2, (p.H - h0) / 64);
   const int nkb = (ke + KB - 1) / KB;
-  const int brows = RES ? ke : KB;                       // expert rows of a feature group of B
-  const int part_b = 2 * brows * 128;
+  const int part_b = 2 * ke * 128;  // RES: bytes of a part of B
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NA; ++i) {
@@ -533,79 +543,116 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   float odd = 0.f;  // NaN once a produced value was not finite
 
   if (warp == 0) {
-    if (lane == 0) {  // ------------------------------------------------ A and B blocks
-      const long long limit = TIMEOUT_CYCLES;
+    if (lane == 0) {  // ------------------------------------------------ A and B parts
       bool ok = true;
-      int kc = 0;
+      int it = 0, s = 0;  // slots filled, the next one
+      uint32_t ph = 1;
+      auto acquire = [&](uint32_t bytes) {
+        ok = mbar_wait(empty + 8 * s, ph, abort_flag);
+        if (ok) mbar_expect_tx(full + 8 * s, bytes);
+        return ok;
+      };
+      auto advance = [&] {
+        ++it;
+        if (++s == NA) s = 0, ph ^= 1;
+      };
       if constexpr (RES) {
-        mbar_expect_tx(wfull, 2 * nbox * ke * 128);
-        for (int q = 0; q < 2; ++q)
+        mbar_expect_tx(wfull, 3 * nbox * ke * 128);
+        for (int q = 0; q < 3; ++q)
           for (int i = 0; i < nbox; ++i)
             tma_load_2d(smem_u32(sB + q * part_b + i * ke * 128), &tm_w, wfull, h0 + 64 * i,
                         q * ke);
       }
       for (int t = first; t < tiles && ok; t += p.per_group)
-        for (int kb = 0; kb < nkb; ++kb, ++kc) {
-          const int s = kc % NA;
-          ok = mbar_wait(empty + 8 * s, ((kc / NA) & 1) ^ 1, abort_flag);
-          if (!ok) break;
-          const uint32_t a = smem_u32(sA + s * A_BYTES), fb = full + 8 * s;
-          mbar_expect_tx(fb, A_BYTES + (RES ? 0 : nbox * 2 * KB * 128));
-          for (int q = 0; q < 2; ++q) {
-            if (side_by_side(p.E))
-              tma_load_2d(a + q * A_PART, &tm_d, fb, q * part_cols(p.E), t * TM);
-            else
-              tma_load_4d(a + q * A_PART, &tm_d, fb, 0, 0, block_at(p.E, q, kb), t * (TM / 32));
-          }
-          if constexpr (!RES) {
-            for (int q = 0; q < 2; ++q)
+        for (int kb = 0; kb < nkb && ok; ++kb) {
+          if constexpr (!RES)
+            for (int q = 0; q < 3 && acquire(nbox * KB * 128); ++q, advance())
               for (int i = 0; i < nbox; ++i)
-                tma_load_2d(smem_u32(sB + s * B_BLOCK + q * part_b + i * KB * 128), &tm_w, fb,
+                tma_load_2d(smem_u32(sRing + s * SLOT + i * KB * 128), &tm_w, full + 8 * s,
                             h0 + 64 * i, q * ke + kb * KB);
+          for (int q = 0; ok && q < PARTS && acquire(SLOT); ++q, advance()) {
+            const uint32_t a = smem_u32(sRing + s * SLOT), fb = full + 8 * s;
+            if (side_by_side(p.E))
+              tma_load_2d(a, &tm_d, fb, q * part_cols(p.E), t * TM);
+            else
+              tma_load_4d(a, &tm_d, fb, 0, 0, block_at(p.E, q, kb), t * (TM / 32));
           }
         }
       if (!ok) *abort_flag = 1;
-      const long long deadline = clock64() + limit;
+      const long long deadline = clock64() + TIMEOUT_CYCLES;
       if constexpr (RES) mbar_drain(wfull, 0, deadline);
-      for (int s = 0; s < NA && s < kc; ++s) {
-        const int last = kc - 1 - ((kc - 1 - s) % NA);
-        mbar_drain(full + 8 * s, (last / NA) & 1, deadline);
+      for (int i = 0; i < NA && i < it; ++i) {
+        const int last = it - 1 - ((it - 1 - i) % NA);
+        mbar_drain(full + 8 * i, (last / NA) & 1, deadline);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {  // ------------------------------------------------ MMAs
+    {  // ------------------------------------------------------------ MMAs
+      const bool leader = elect_one();
       const uint32_t idesc = idesc_bf16(64 * nbox, false, true);
-      const uint64_t ad0 = sdesc(smem_u32(sA), 16, 1024);
-      const uint64_t bd0 = sdesc(smem_u32(sB), brows * 128, 1024);
-      int n = 0, kc = 0;
+      const uint64_t ad0 = sdesc(smem_u32(sRing), 16, 1024);
+      const uint64_t bd0 = RES ? sdesc(smem_u32(sB), ke * 128, 1024)
+                               : sdesc(smem_u32(sRing), KB * 128, 1024);
+      int n = 0, s = 0;
+      uint32_t ph = 0;
       bool ok = true;
-      if constexpr (RES) ok = mbar_wait(wfull, 0, abort_flag);
+      auto arrived = [&] {  // the next slot of the ring
+        ok = mbar_wait_all(full + 8 * s, ph, abort_flag);
+        if (ok) tc_fence_after();
+        return ok;
+      };
+      auto advance = [&] {
+        if (++s == NA) s = 0, ph ^= 1;
+      };
+      if constexpr (RES) ok = mbar_wait_all(wfull, 0, abort_flag);
       for (int t = first; t < tiles && ok; t += p.per_group, ++n) {
-        ok = mbar_wait(tempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, abort_flag);
+        ok = mbar_wait_all(tempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, abort_flag);
         if (!ok) break;
+        tc_fence_after();
         const uint32_t d = tmem + (n & 1) * NH;
-        for (int kb = 0; kb < nkb; ++kb, ++kc) {
-          const int s = kc % NA;
-          ok = mbar_wait(full + 8 * s, (kc / NA) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a = ad0 + ((s * A_BYTES) >> 4);
-          const uint64_t b = bd0 + ((RES ? kb * KB * 128 : s * B_BLOCK) >> 4);
-          const int steps = min(KB / 16, ke / 16 - kb * (KB / 16));
-          for (int ks = 0; ks < steps; ++ks) {
-            const uint64_t ah = a + ((ks * 32) >> 4), am = ah + (A_PART >> 4);
-            const uint64_t bh = b + ((ks * 2048) >> 4), bm = bh + (part_b >> 4);
-            umma_bf16(d, ah, bh, idesc, kb > 0 || ks > 0 ? 1u : 0u);
-            umma_bf16(d, ah, bm, idesc, 1u);
-            umma_bf16(d, am, bh, idesc, 1u);
+        for (int kb = 0; kb < nkb && ok; ++kb) {
+          uint64_t b[3];
+          int sb[3];
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            if constexpr (RES) {
+              b[q] = bd0 + ((q * part_b + kb * KB * 128) >> 4);
+            } else {
+              if (!ok || !arrived()) break;
+              sb[q] = s;
+              b[q] = bd0 + ((s * SLOT) >> 4);
+              advance();
+            }
           }
-          umma_commit(empty + 8 * s);
+          const int steps = min(KB / 16, ke / 16 - kb * (KB / 16));
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q) {  // dlogit's part q by w's parts 0 to 2 - q
+            if (!ok || !arrived()) break;
+            if (leader) {
+              const uint64_t a = ad0 + ((s * SLOT) >> 4);
+#pragma unroll
+              for (int r = 0; r < 3 - q; ++r)
+                for (int ks = 0; ks < steps; ++ks)
+                  umma_bf16(d, a + ((ks * 32) >> 4), b[r] + ((ks * 2048) >> 4), idesc,
+                            kb > 0 || q > 0 || r > 0 || ks > 0 ? 1u : 0u);
+              umma_commit(empty + 8 * s);
+            }
+            __syncwarp();
+            advance();
+          }
+          if constexpr (!RES)
+            if (ok && leader)
+              for (int q = 0; q < 3; ++q) umma_commit(empty + 8 * sb[q]);
         }
-        if (ok) umma_commit(tfull + 8 * (n & 1));
+        if (ok && leader) umma_commit(tfull + 8 * (n & 1));
+        __syncwarp();
       }
       if (!ok) *abort_flag = 1;
-      umma_commit(done);
-      mbar_drain(done, 0, clock64() + TIMEOUT_CYCLES);
+      if (leader) {
+        umma_commit(done);
+        mbar_drain(done, 0, clock64() + TIMEOUT_CYCLES);
+      }
+      __syncwarp();
     }
   } else if (warp == 2) {
     if (lane == 0) {  // ------------------------------------------------ dx_in boxes
@@ -738,14 +785,14 @@ usaf_status launch_w(const CUtensorMap& d, const CUtensorMap& x, const gw::Param
   return launch_dep(router_grad_w_tc_kernel<STACK>, grid, gw::THREADS, C::SMEM, st, d, x, p);
 }
 
-template <bool RES>
+template <bool RES, bool STACK>
 usaf_status launch_x(const CUtensorMap& d, const CUtensorMap& w, const CUtensorMap& in,
                      const CUtensorMap& out, const gx::Params& p, unsigned grid, cudaStream_t st) {
   USAF_TRACE("router_grad_x", st);
   static OncePerDevice once;
-  if (!grow_smem(once, router_grad_x_tc_kernel<RES>, gx::SMEM_MAX)) return USAF_ERR_CUDA;
-  const int smem = p.ring * gx::A_BYTES + p.slots * gx::BOX + gx::b_bytes(p.ke) + 1024 + 512;
-  return launch_dep(router_grad_x_tc_kernel<RES>, dim3(grid), gx::THREADS, smem, st, d, w, in, out,
+  if (!grow_smem(once, router_grad_x_tc_kernel<RES, STACK>, gx::SMEM_MAX)) return USAF_ERR_CUDA;
+  const int smem = p.ring * gx::SLOT + p.slots * gx::BOX + gx::b_bytes(p.ke) + gx::EXTRA;
+  return launch_dep(router_grad_x_tc_kernel<RES, STACK>, dim3(grid), gx::THREADS, smem, st, d, w, in, out,
                     p);
 }
 
@@ -761,7 +808,7 @@ int64_t stretch(int64_t T, int64_t E, int64_t H) {
 
 void router_grad_tc_layout(int64_t T, int64_t E, int64_t H, Carver& c, RouterGradWs& w) {
   w.parts = c.take<uint16_t>(parts_size(T, (int)E));
-  w.w_parts = c.take<uint16_t>(2 * w_rows((int)E) * H);
+  w.w_parts = c.take<uint16_t>(3 * w_rows((int)E) * H);
   const int64_t s = ceil_div(T, stretch(T, E, H));
   w.g_part = c.take<float>(s > 1 ? s * E * H : 1);
 }
@@ -811,7 +858,7 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
   const uint32_t wrows = ke <= gx::MAX_RES ? ke : gx::KB;
   const int64_t groups = ceil_div(H, gx::NH), tiles = ceil_div(a.T, gx::TM);
   if (!map_parts(&d, parts, a.T, E, 1, gx::TM) ||
-      !map_bf16_2d(&w, wparts, H, 2 * ke, 64, wrows) ||
+      !map_bf16_2d(&w, wparts, H, 3 * ke, 64, wrows) ||
       !map_bf16_2d(&out, a.dx, H, a.T, 64, gx::TM) ||
       !map_bf16_2d(&in, a.dx_in ? a.dx_in : a.dx, H, a.T, 64, gx::TM))
     return USAF_ERR_CUDA;
@@ -832,8 +879,9 @@ usaf_status router_grad_tc(const RouterGradArgs& a, const RouterGradWs& ws, cuda
   if (most < 1) most = 1;
   p.per_group = (int)(most < tiles ? most : tiles);
   const unsigned grid = (unsigned)(groups * p.per_group);
-  return ke <= gx::MAX_RES ? launch_x<true>(d, w, in, out, p, grid, st)
-                           : launch_x<false>(d, w, in, out, p, grid, st);
+  if (stacked(E)) return launch_x<true, true>(d, w, in, out, p, grid, st);
+  return ke <= gx::MAX_RES ? launch_x<true, false>(d, w, in, out, p, grid, st)
+                           : launch_x<false, false>(d, w, in, out, p, grid, st);
 }
 
 }  // namespace usaf

@@ -48,3 +48,28 @@ def test_router_grad_calls_in_a_row_on_one_workspace(T, E, H):
         for a, b in zip(alone, row):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert torch.isfinite(alone[0][0]).all() and torch.isfinite(alone[0][1].float()).all()
+
+
+@pytest.mark.parametrize("E,apart", [(8, 2.0 ** -14), (40, 2.0 ** -13), (64, 2.0 ** -12),
+                                     (128, 2.0 ** -12), (160, 2.0 ** -12), (250, 2.0 ** -12)])
+def test_dx_of_router_rows_that_share_a_component(E, apart):
+    """Rows of w_router that differ by little from what they share, under a softmax's gradient, whose
+    rows sum to zero: the shared part cancels, and what is left has to be as good as an fp32 sum.
+    With terms = sum |dlogit| |w|: products left out 3 u of them; the sums, at most 6 E / 16
+    additions, each within 2 u of an accumulator that wanders about terms / sqrt(E), below 13 u.
+    So 16 u of terms in norm, and the rounding of the result to bf16, 2^-9."""
+    dev = device()
+    T, H = 300, 256
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((T, E))
+    p = np.exp(l) / np.exp(l).sum(1, keepdims=True)
+    a = rng.standard_normal((T, E))
+    dl = (p * (a - (p * a).sum(1, keepdims=True))).astype(np.float32)
+    w = (1.0 + apart * rng.standard_normal((E, H))).astype(np.float32)
+    dx = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    B.router_grad(to_dev(dl, dev), None, to_dev(w, dev), dx=dx)
+    _, ref = TO.router_grad(dl, np.zeros((T, 1)), w)
+    terms = np.abs(dl.astype(np.float64)) @ np.abs(w)
+    bound = 2.0 ** -9 + 16 * 2.0 ** -24 * np.linalg.norm(terms) / np.linalg.norm(ref)
+    err = rel_l2(dx.float().cpu().numpy(), ref)
+    assert err <= bound, (err, bound)
