@@ -14,8 +14,9 @@ status words, so every replica applies the same update or skips the same step.
 
 Two additions to the step, both off unless asked for (see include/usaf_train.h):
 - a load-balance loss and a z-loss on the router's logits (balance_coef, z_coef): their gradient
-  joins the router's gradient and dx. Under data parallelism each rank adds the loss of its own
-  tokens, and the ranks' gradients are summed like the rest;
+  joins the router's gradient and dx. A call's loss is a mean over its tokens; where a step is cut
+  into micro-batches or spread over ranks, whose gradients are summed, each call's loss enters with
+  its share of the step (aux_share), so that the coefficients mean the same however it is cut;
 - activations in 8 bits (save_act8 / restore_act8) between a forward and its backward, so that
   layers can share the buffers a forward leaves (share_activations; StackTrainer(act8=True)).
 """
@@ -111,6 +112,9 @@ class MoELayer:
         self.balance_coef, self.z_coef = float(balance_coef), float(z_coef)
         self.aux = self.balance_coef != 0.0 or self.z_coef != 0.0
         self._graphs = {}
+        self._shares = {}
+        if self.aux:
+            self.aux_share()  # made here: a captured step may not allocate it
         self.set_sequences()
         # router SparseAdam state (dense over all E*H entries)
         self.r_p = self.w_router.reshape(-1).clone()
@@ -200,10 +204,21 @@ class MoELayer:
                          token_mask=self.token_mask, group_offset=self.group_offset,
                          dev_status=dev_status, ws=self.ws_aux, stream=stream)
 
-    def _aux_backward(self, x, dx, stream=None, dev_status=None):
-        """Adds the losses' gradient to g_router and, unless None, dx."""
+    def aux_share(self, micro_batches=1):
+        """What one call's losses count for in a step of that many equal micro-batches on every rank
+        of the layer's group: a device tensor [1], or None for the whole of it."""
+        n = int(micro_batches)
+        if self.group is not None:
+            import torch.distributed as dist
+            n *= dist.get_world_size(self.group)
+        if n not in self._shares:
+            self._shares[n] = None if n == 1 else torch.full((1,), 1.0 / n, device=self.dev)
+        return self._shares[n]
+
+    def _aux_backward(self, x, dx, stream=None, dev_status=None, share=None):
+        """Adds the losses' gradient, times `share` [1] (None: 1), to g_router and, unless None, dx."""
         B.router_aux_bwd(self.logits, self.k, self.aux_count, self.aux_n, self.dlogit_aux,
-                         self.balance_coef, self.z_coef, token_mask=self.token_mask,
+                         self.balance_coef, self.z_coef, d_loss=share, token_mask=self.token_mask,
                          group_offset=self.group_offset, dev_status=dev_status, stream=stream)
         B.router_grad(self.dlogit_aux, x, self.w_router, g_router=self.g_router,
                       g_in=self.g_router, dx=dx, dx_in=dx, dev_status=dev_status,
@@ -315,10 +330,12 @@ class MoELayer:
         self._check_tokens(x=x, dy=dy, dx=dx)
         self.backward_into(x, dy, accumulate=0, dx=dx if want_dx else None, stream=stream)
 
-    def backward_into(self, x, dy, accumulate=0, dx=None, stream=None, dev_status=None):
+    def backward_into(self, x, dy, accumulate=0, dx=None, stream=None, dev_status=None,
+                      aux_share=None):
         """The sparse backward with this set's masked-gradient plan; accumulate = 1 adds into
         g_act and g_router (micro-batches). With auxiliary losses on, their gradient joins
-        g_router and dx."""
+        g_router and dx, times aux_share (a device tensor [1]; None: this call is its rank's whole
+        step)."""
         status = self.status if dev_status is None else dev_status
         B.moe_bwd_sparse_planned(self.s, x, self.w_router, self.w_gate_up, self.w_down, self.rt,
                                  self.x_perm, self.h, self.wa, dy, self.act, self.g_act,
@@ -327,7 +344,8 @@ class MoELayer:
                                  renorm=self.renorm, dev_status=status, ws=self.ws_bwd,
                                  stream=stream)
         if self.aux:
-            self._aux_backward(x, dx, stream, status)
+            share = self.aux_share() if aux_share is None else aux_share
+            self._aux_backward(x, dx, stream, status, share)
 
     def optimizer_step(self, stream=None, skip_if_nonfinite=1):
         """Router update on the calling stream (the next routing reads it); expert update on the

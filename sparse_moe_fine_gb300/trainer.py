@@ -100,14 +100,15 @@ class StackTrainer:
             x = y
         return inputs
 
-    def _backward(self, inputs, dy, first, dense):
+    def _backward(self, inputs, dy, first, dense, micro_batches):
         for i in reversed(range(len(self.layers))):
             L = self.layers[i]
             x = inputs[i]
             if self.act8 and i < len(self.layers) - 1:
                 x = L.restore_act8(self._stores[i], self._x8[self._key[i]])
             dx = L.dx if i > 0 else None  # the bottom layer's input needs no gradient
-            L.backward_into(x, dy, accumulate=0 if first else 1, dx=dx)
+            L.backward_into(x, dy, accumulate=0 if first else 1, dx=dx,
+                            aux_share=L.aux_share(micro_batches) if L.aux else None)
             if dense:
                 # the importance phase's dense gradient of this micro-batch, accumulated, from
                 # the dh and permuted dy the sparse call just left in the layer's workspace
@@ -120,7 +121,8 @@ class StackTrainer:
     # ------------------------------------------------------------------ one optimizer step
     def step(self, x_micro, dy_micro):
         """One optimizer step over the micro-batches: x_micro[j] [T,H] is micro-batch j's input
-        to the bottom layer, dy_micro[j] [T,H] the gradient at the top layer's output."""
+        to the bottom layer, dy_micro[j] [T,H] the gradient at the top layer's output. The
+        layers' gradients are summed over the micro-batches, their auxiliary losses averaged."""
         if len(x_micro) != len(dy_micro) or not x_micro:
             raise ValueError("need the same number (>= 1) of inputs and upstream gradients")
         self.step_no += 1
@@ -132,7 +134,7 @@ class StackTrainer:
             L.status.zero_()
         for j, (x, dy) in enumerate(zip(x_micro, dy_micro)):
             inputs = self._forward(x)
-            self._backward(inputs, dy, first=(j == 0), dense=dense)
+            self._backward(inputs, dy, first=(j == 0), dense=dense, micro_batches=len(x_micro))
         status = []
         for L in self.layers:
             L.lr = lr

@@ -10,6 +10,9 @@ import torch
 
 from oracle import train_oracle as TO
 from sparse_moe_fine_gb300 import binding as B
+from sparse_moe_fine_gb300 import synth
+from sparse_moe_fine_gb300.layer import MoELayer
+from sparse_moe_fine_gb300.trainer import StackTrainer
 
 from _gpu import device, rel_l2, to_dev
 
@@ -73,3 +76,37 @@ def test_dx_of_router_rows_that_share_a_component(E, apart):
     bound = 2.0 ** -9 + 16 * 2.0 ** -24 * np.linalg.norm(terms) / np.linalg.norm(ref)
     err = rel_l2(dx.float().cpu().numpy(), ref)
     assert err <= bound, (err, bound)
+
+
+def _layers(dev, cfg, T, n, seed=60, **kw):
+    """n layers for T tokens with the weights of `cfg`'s inputs, whatever T is."""
+    out = []
+    for i in range(n):
+        inp = synth.moe_inputs(cfg, seed=seed + i)
+        t = lambda a: torch.from_numpy(a).to(dev).to(torch.bfloat16 if cfg.bf16 else torch.float32)
+        act = torch.from_numpy(synth.uniform_mask(cfg.N, cfg.K, seed=seed + i)).to(dev)
+        out.append(MoELayer(T, cfg.H, cfg.E, cfg.k, cfg.I, t(inp["w_gate_up"]), t(inp["w_down"]),
+                            torch.from_numpy(inp["w_router"]).to(dev), act, device=dev, **kw))
+    return out
+
+
+CFG = synth.small_config("aux_paths", T=256, H=128, E=8, k=2, I=128, bf16=True, frac=0.05)
+
+
+@pytest.mark.parametrize("M", [2, 4])
+def test_a_batch_cut_into_micro_batches_has_the_whole_batchs_loss_gradient(M):
+    """No upstream gradient, so the router's gradient is the losses' alone. The cut batch's sequences
+    are the micro-batches. fp32 results of the same terms: 1e-5 in norm each way, with the logits'."""
+    dev = device()
+    T = CFG.T
+    x = to_dev(synth.moe_inputs(CFG, seed=3)["x"], dev, True)
+    zero = torch.zeros_like(x)
+    whole, = _layers(dev, CFG, T, 1, balance_coef=2.0, z_coef=0.5)
+    whole.set_sequences(torch.arange(0, T + 1, T // M, dtype=torch.int32, device=dev))
+    StackTrainer([whole], total_steps=10, reselect_every=0).step([x], [zero])
+    cut, = _layers(dev, CFG, T // M, 1, balance_coef=2.0, z_coef=0.5)
+    StackTrainer([cut], total_steps=10, reselect_every=0).step(list(x.split(T // M)),
+                                                               list(zero.split(T // M)))
+    torch.cuda.synchronize()
+    a, b = whole.g_router.cpu().numpy(), cut.g_router.cpu().numpy()
+    assert np.linalg.norm(a) > 0 and rel_l2(b, a) <= 4e-5
