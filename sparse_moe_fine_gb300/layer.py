@@ -115,6 +115,9 @@ class MoELayer:
         self._shares = {}
         if self.aux:
             self.aux_share()  # made here: a captured step may not allocate it
+            self.dlogit_aux = torch.empty(T, E, device=d)
+            self.ws_rgrad = torch.empty(B.router_grad_workspace_size(T, E, H, self.dtype),
+                                        dtype=torch.uint8, device=d)
         self.set_sequences()
         # router SparseAdam state (dense over all E*H entries)
         self.r_p = self.w_router.reshape(-1).clone()
@@ -170,39 +173,49 @@ class MoELayer:
         part of a checkpoint. With the
         losses on: aux_count and aux_prob [G,E], aux_n [G] and aux_loss [3] (total, balance, z) hold
         the last forward's values."""
+        self._check_sequences(group_offset, token_mask)
         if not self.aux:
-            if group_offset is not None or token_mask is not None:
-                raise ValueError("sequences are only for the auxiliary losses, which are off")
             return
         d, T, E = self.dev, self.T, self.E
-        for name, t, dt in (("group_offset", group_offset, torch.int32),
-                            ("token_mask", token_mask, torch.uint8)):
-            if t is None:
-                continue
-            if t.dtype != dt or not t.is_cuda or not t.is_contiguous() or t.dim() != 1:
-                raise ValueError(f"{name}: expected a contiguous one-dimensional CUDA {dt} tensor")
-        if token_mask is not None and token_mask.numel() != T:
-            raise ValueError(f"token_mask: expected {T} entries, got {token_mask.numel()}")
-        if group_offset is not None and group_offset.numel() < 2:
-            raise ValueError("group_offset needs at least two entries")
         G = 1 if group_offset is None else group_offset.numel() - 1
         self.group_offset, self.token_mask = group_offset, token_mask
         self.aux_count = torch.zeros(G, E, dtype=torch.int32, device=d)
         self.aux_prob = torch.zeros(G, E, device=d)
         self.aux_n = torch.zeros(G, dtype=torch.int32, device=d)
         self.aux_loss = torch.zeros(3, device=d)
-        self.dlogit_aux = torch.empty(T, E, device=d)
         self.ws_aux = torch.empty(B.router_aux_workspace_size(T, E, self.k, G), dtype=torch.uint8,
                                   device=d)
-        self.ws_rgrad = torch.empty(B.router_grad_workspace_size(T, E, self.H, self.dtype),
-                                    dtype=torch.uint8, device=d)
         self._graphs = {}  # captured steps hold the old buffers' pointers
+
+    def _check_sequences(self, group_offset, token_mask):
+        if not self.aux and (group_offset is not None or token_mask is not None):
+            raise ValueError("sequences are only for the auxiliary losses, which are off")
+        for name, t, dt in (("group_offset", group_offset, torch.int32),
+                            ("token_mask", token_mask, torch.uint8)):
+            if t is None:
+                continue
+            if t.dtype != dt or not t.is_cuda or not t.is_contiguous() or t.dim() != 1:
+                raise ValueError(f"{name}: expected a contiguous one-dimensional CUDA {dt} tensor")
+        if token_mask is not None and token_mask.numel() != self.T:
+            raise ValueError(f"token_mask: expected {self.T} entries, got {token_mask.numel()}")
+        if group_offset is not None and group_offset.numel() < 2:
+            raise ValueError("group_offset needs at least two entries")
 
     def _aux_forward(self, stream=None, dev_status=None):
         B.router_aux_fwd(self.logits, self.rt.topk_idx, self.k, self.aux_count, self.aux_prob,
                          self.aux_n, self.aux_loss, self.balance_coef, self.z_coef,
                          token_mask=self.token_mask, group_offset=self.group_offset,
                          dev_status=dev_status, ws=self.ws_aux, stream=stream)
+
+    def live_tokens(self, group_offset=None, token_mask=None):
+        """Tokens that a mask and sequences leave to the losses, as a device tensor of no axes (a token
+        whose logits are all -inf counts here; the losses leave it out)."""
+        live = (torch.ones(self.T, dtype=torch.bool, device=self.dev) if token_mask is None
+                else token_mask != 0)
+        if group_offset is not None:
+            t = torch.arange(self.T, device=self.dev)
+            live = live & (t >= group_offset[0]) & (t < group_offset[-1])
+        return live.sum()
 
     def aux_share(self, micro_batches=1):
         """What one call's losses count for in a step of that many equal micro-batches on every rank

@@ -100,7 +100,7 @@ class StackTrainer:
             x = y
         return inputs
 
-    def _backward(self, inputs, dy, first, dense, micro_batches):
+    def _backward(self, inputs, dy, first, dense, share):
         for i in reversed(range(len(self.layers))):
             L = self.layers[i]
             x = inputs[i]
@@ -108,7 +108,7 @@ class StackTrainer:
                 x = L.restore_act8(self._stores[i], self._x8[self._key[i]])
             dx = L.dx if i > 0 else None  # the bottom layer's input needs no gradient
             L.backward_into(x, dy, accumulate=0 if first else 1, dx=dx,
-                            aux_share=L.aux_share(micro_batches) if L.aux else None)
+                            aux_share=share(L) if L.aux else None)
             if dense:
                 # the importance phase's dense gradient of this micro-batch, accumulated, from
                 # the dh and permuted dy the sparse call just left in the layer's workspace
@@ -119,12 +119,36 @@ class StackTrainer:
             dy = L.dx
 
     # ------------------------------------------------------------------ one optimizer step
-    def step(self, x_micro, dy_micro):
+    def _shares(self, sequences):
+        """Each micro-batch's share of the step's auxiliary losses: its tokens' share of the tokens of
+        all of them, on all ranks."""
+        L = next(L for L in self.layers if L.aux)
+        n = torch.stack([L.live_tokens(*s) for s in sequences]).float()
+        total = n.sum()
+        if L.group is not None:
+            torch.distributed.all_reduce(total, group=L.group)
+        return (n / total.clamp(min=1.0)).split(1)
+
+    def step(self, x_micro, dy_micro, sequences=None):
         """One optimizer step over the micro-batches: x_micro[j] [T,H] is micro-batch j's input
         to the bottom layer, dy_micro[j] [T,H] the gradient at the top layer's output. The
-        layers' gradients are summed over the micro-batches, their auxiliary losses averaged."""
+        layers' gradients are summed over the micro-batches, their auxiliary losses averaged.
+        sequences[j]: micro-batch j's (group_offset, token_mask) as MoELayer.set_sequences takes them,
+        for every layer with auxiliary losses (the last one's stay set); a micro-batch then counts by
+        its tokens (data parallel: on every rank or on none). Without it the layers' own sequences hold for every micro-batch, and micro-batches
+        and ranks count alike."""
         if len(x_micro) != len(dy_micro) or not x_micro:
             raise ValueError("need the same number (>= 1) of inputs and upstream gradients")
+        if sequences is not None:
+            if len(sequences) != len(x_micro):
+                raise ValueError("need one (group_offset, token_mask) per micro-batch")
+            if not any(L.aux for L in self.layers):
+                raise ValueError("sequences are only for the auxiliary losses, which are off")
+            for L in self.layers:
+                for s in sequences:
+                    if L.aux:
+                        L._check_sequences(*s)
+            shares = self._shares(sequences)
         self.step_no += 1
         n = self.step_no
         lr = cosine_lr(n, self.total_steps, self.lr_peak, self.warmup_steps)
@@ -133,8 +157,14 @@ class StackTrainer:
             L.status = L.status2[L.step_count % 2:L.step_count % 2 + 1]
             L.status.zero_()
         for j, (x, dy) in enumerate(zip(x_micro, dy_micro)):
+            share = lambda L: L.aux_share(len(x_micro))
+            if sequences is not None:
+                share = lambda L, s=shares[j]: s
+                for L in self.layers:
+                    if L.aux:
+                        L.set_sequences(*sequences[j])
             inputs = self._forward(x)
-            self._backward(inputs, dy, first=(j == 0), dense=dense, micro_batches=len(x_micro))
+            self._backward(inputs, dy, first=(j == 0), dense=dense, share=share)
         status = []
         for L in self.layers:
             L.lr = lr

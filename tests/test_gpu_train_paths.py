@@ -110,3 +110,27 @@ def test_a_batch_cut_into_micro_batches_has_the_whole_batchs_loss_gradient(M):
     torch.cuda.synchronize()
     a, b = whole.g_router.cpu().numpy(), cut.g_router.cpu().numpy()
     assert np.linalg.norm(a) > 0 and rel_l2(b, a) <= 4e-5
+
+
+def test_micro_batches_of_their_own_sequences():
+    """A packed, masked batch in one call, and cut in two with a packing and a mask for each half: the
+    same gradient, 4e-5 in norm as above. The halves differ in sequences and in tokens."""
+    dev = device()
+    T, h = CFG.T, CFG.T // 2
+    x = to_dev(synth.moe_inputs(CFG, seed=4)["x"], dev, True)
+    zero = torch.zeros_like(x)
+    mask = (torch.arange(T, device=dev) % 5 != 0).to(torch.uint8)
+    mask[h:h + 90] = 0
+    offs = [[0, 11, 50, h], [0, 100, h]]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+    whole, = _layers(dev, CFG, T, 1, balance_coef=2.0, z_coef=0.5)
+    whole.set_sequences(i32(offs[0] + [h + o for o in offs[1][1:]]), mask)
+    StackTrainer([whole], total_steps=10, reselect_every=0).step([x], [zero])
+    cut, = _layers(dev, CFG, h, 1, balance_coef=2.0, z_coef=0.5)
+    tr = StackTrainer([cut], total_steps=10, reselect_every=0)
+    tr.step(list(x.split(h)), list(zero.split(h)),
+            sequences=[(i32(o), m.contiguous()) for o, m in zip(offs, mask.split(h))])
+    torch.cuda.synchronize()
+    a, b = whole.g_router.cpu().numpy(), cut.g_router.cpu().numpy()
+    assert np.linalg.norm(a) > 0 and rel_l2(b, a) <= 4e-5
+    assert cut.aux_count.shape[0] == 2 and int(cut.status.item()) == 0
