@@ -43,6 +43,7 @@ extern "C" {
  *                offsets are clamped)
  * A term whose coefficient is 0 is still reported in loss[1] / loss[2] and adds nothing to loss[0].
  * All sums have a fixed order: the same inputs give the same bits.
+ * The workspace must be 16-byte aligned (INVALID_ARG otherwise).
  * Limits: T >= 1, 1 <= k <= min(E, 32), E <= 1024, 1 <= G <= 2^20, T*k < 2^31 - 65536.
  * Errors: INVALID_ARG, WORKSPACE, CUDA.
  * ------------------------------------------------------------------------------------------- */

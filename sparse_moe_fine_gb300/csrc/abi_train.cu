@@ -86,6 +86,7 @@ usaf_status usaf_router_aux_fwd(int64_t T, int64_t E, int64_t k, const float* lo
                     coef_z, dev_status));
   if (!topk_idx || !count || !prob_sum || !n_tok || !loss) return USAF_ERR_INVALID_ARG;
   if (!ws || ws_bytes < usaf_router_aux_workspace_size(T, E, k, G)) return USAF_ERR_WORKSPACE;
+  if (!aligned16(ws)) return USAF_ERR_INVALID_ARG;
   a.topk_idx = topk_idx;
   Carver c(ws);
   AuxWs w;
