@@ -214,10 +214,9 @@ class Routing:
                        torch.empty(cap, **i32), torch.empty(cap, **i32), torch.empty(R, **i32))
 
     def c(self) -> _Routing:
-        return _Routing(self.topk_idx.data_ptr(), self.topk_w.data_ptr(),
-                        self.expert_count.data_ptr(), self.expert_offset.data_ptr(),
-                        self.perm_tok.data_ptr(), self.perm_slot.data_ptr(),
-                        self.slot_row.data_ptr())
+        return _Routing(_ptr(self.topk_idx), _ptr(self.topk_w), _ptr(self.expert_count),
+                        _ptr(self.expert_offset), _ptr(self.perm_tok), _ptr(self.perm_slot),
+                        _ptr(self.slot_row))
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
