@@ -574,7 +574,11 @@ def _ok_rows(name, t, dtype, shape, dev):
 
 
 def _on(stream, dev):
-    """The stream handle: the device's current stream unless one is given."""
+    """The stream handle: the device's current stream unless one is given. The library launches on
+    the current device, so the tensors have to be there."""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on CUDA device {dev}, but the current one is "
+                         f"{torch._C._cuda_getDevice()}: call within torch.cuda.device({dev})")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
