@@ -573,6 +573,28 @@ def _ok_rows(name, t, dtype, shape, dev):
     return t.data_ptr(), (ld if ld >= n else n)
 
 
+def _buf(name, t, dev, least=1, dtype=None):
+    """The address of a contiguous buffer of at least `least` entries (bytes where no dtype is
+    given); None and bare addresses pass."""
+    if t is None or isinstance(t, int):
+        return t
+    n = t.numel() * (1 if dtype else t.element_size())
+    if (n < least or t.get_device() != dev or not t.is_contiguous()
+            or (dtype is not None and t.dtype is not dtype)):
+        raise ValueError(f"{name}: expected at least {least} {dtype or 'bytes'}, contiguous, on CUDA "
+                         f"device {dev}, got {list(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _status(t, dev):
+    return _buf("dev_status", t, dev, 4)
+
+
+def _ws_buf(ws, dev):
+    """The address and size in bytes of a workspace."""
+    return _buf("ws", ws, dev), ws.numel() * ws.element_size()
+
+
 def _on(stream, dev):
     """The stream handle: the device's current stream unless one is given. The library launches on
     the current device, so the tensors have to be there."""
@@ -618,8 +640,8 @@ def router_aux_fwd(logits, topk_idx, k, count, prob_sum, n_tok, loss, coef_balan
         _opt("token_mask", token_mask, _u8, (T,), d),
         _opt("group_offset", group_offset, _i32, (G + 1,), d), G, float(coef_balance),
         float(coef_z), _ok("count", count, _i32, ge, d), _ok("prob_sum", prob_sum, _f32, ge, d),
-        _ok("n_tok", n_tok, _i32, (G,), d), _ok("loss", loss, _f32, (3,), d), _ptr(dev_status),
-        ws.data_ptr(), ws.numel(), _on(stream, d)))
+        _ok("n_tok", n_tok, _i32, (G,), d), _ok("loss", loss, _f32, (3,), d), _status(dev_status, d),
+        *_ws_buf(ws, d), _on(stream, d)))
 
 
 def router_aux_bwd(logits, k, count, n_tok, dlogit, coef_balance, coef_z, d_loss=None,
@@ -637,7 +659,7 @@ def router_aux_bwd(logits, k, count, n_tok, dlogit, coef_balance, coef_z, d_loss
         T, E, int(k), lp, ld, _opt("token_mask", token_mask, _u8, (T,), d),
         _opt("group_offset", group_offset, _i32, (G + 1,), d), G, float(coef_balance),
         float(coef_z), _ok("count", count, _i32, (G, E), d), _ok("n_tok", n_tok, _i32, (G,), d),
-        _opt("d_loss", d_loss, _f32, (1,), d), op, ldo, int(accumulate), _ptr(dev_status),
+        _opt("d_loss", d_loss, _f32, (1,), d), op, ldo, int(accumulate), _status(dev_status, d),
         _on(stream, d)))
 
 
@@ -664,7 +686,7 @@ def router_grad(dlogit, x, w_router, g_router=None, g_in=None, dx=None, dx_in=No
         T, E, H, _dt(ref), dp, ld, _opt("x", x, dt, th, d),
         _opt("w_router", w_router, _f32, eh, d), _opt("g_in", g_in, _f32, eh, d),
         _opt("g_router", g_router, _f32, eh, d), _opt("dx_in", dx_in, dt, th, d),
-        _opt("dx", dx, dt, th, d), _ptr(dev_status), ws.data_ptr(), ws.numel(), _on(stream, d)))
+        _opt("dx", dx, dt, th, d), _status(dev_status, d), *_ws_buf(ws, d), _on(stream, d)))
 
 
 @dataclass
@@ -703,9 +725,10 @@ def act8_save(s: Shape, x, h, rt: Routing, store: ActStore8, dev_status=None, st
     """usaf_act8_save: x [T,H] and h [2I,R_cap] of a forward into the store."""
     d, sh = x.get_device(), ActStore8.shapes(s)
     xp, hp = _ok("x", x, x.dtype, sh[0], d), _ok("h", h, x.dtype, sh[2], d)
+    _buf("expert_offset", rt.expert_offset, d, s.E + 1, _i32)
     r = rt.c()
     _check("usaf_act8_save", lib().usaf_act8_save(
-        ctypes.byref(s), _dt(x), xp, hp, ctypes.byref(r), *store.ptrs(sh, d), _ptr(dev_status),
+        ctypes.byref(s), _dt(x), xp, hp, ctypes.byref(r), *store.ptrs(sh, d), _status(dev_status, d),
         _on(stream, d)))
 
 
@@ -715,6 +738,9 @@ def act8_restore(s: Shape, store: ActStore8, rt: Routing, x_perm, h, wa, x=None,
     d, dt, sh = h.get_device(), h.dtype, ActStore8.shapes(s)
     cap = sh[2][1]
     ptrs = store.ptrs(sh, d)
+    for name, n, kind in (("topk_w", s.T * s.k, _f32), ("expert_offset", s.E + 1, _i32),
+                          ("perm_tok", cap, _i32), ("perm_slot", cap, _i32)):
+        _buf(name, getattr(rt, name), d, n, kind)
     r = rt.c()
     _check("usaf_act8_restore", lib().usaf_act8_restore(
         ctypes.byref(s), _dt(h), *ptrs, ctypes.byref(r), _opt("x", x, dt, sh[0], d),

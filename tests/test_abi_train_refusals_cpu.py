@@ -136,3 +136,44 @@ def test_tensors_of_another_device_are_refused(fake, name):
         with pytest.raises(ValueError):
             call()
     assert len(fake.calls) == 1
+
+
+@pytest.mark.parametrize("name", ["fwd", "grad"])
+def test_workspaces_off_the_device_or_strided_are_refused(fake, name):
+    for bad in (_Tensor((1 << 20,), U8, dev=-1), _Tensor((1 << 20,), U8, dev=1),
+                _Tensor((1 << 20,), U8, contiguous=False)):
+        with pytest.raises(ValueError):
+            _calls(ws=bad)[name]()
+    assert not fake.calls
+    _calls(ws=_Tensor((1 << 18,), I32))[name]()  # its size in bytes counts
+    a = fake.calls[0][1]
+    assert a[-2] == 1 << 20
+
+
+@pytest.mark.parametrize("name", ["fwd", "bwd", "grad", "save"])
+def test_status_words_off_the_device_or_too_small_are_refused(fake, name):
+    for bad in (_Tensor((1,), I32, dev=-1), _Tensor((1,), I32, dev=1), _Tensor((0,), I32),
+                _Tensor((1,), U8)):
+        with pytest.raises(ValueError):
+            _calls(status=bad)[name]()
+    assert not fake.calls
+    _calls(status=_Tensor((1,), I32))[name]()
+    _calls(status=4096)[name]()  # an address
+    assert len(fake.calls) == 2
+
+
+@pytest.mark.parametrize("name,fields", [("save", ["expert_offset"]),
+                                         ("restore", ["topk_w", "expert_offset", "perm_tok",
+                                                      "perm_slot"])])
+def test_routing_tables_of_another_shape_are_refused(fake, name, fields):
+    """Rows are addressed by them: a routing of another shape would be read and written past the ends."""
+    for f in fields:
+        n = getattr(_routing(0), f).numel()
+        dt = torch.float32 if f == "topk_w" else I32
+        for bad in (_Tensor((n - 1,), dt), _Tensor((n,), torch.int64), _Tensor((n,), dt, dev=-1),
+                    _Tensor((n,), dt, contiguous=False)):
+            with pytest.raises(ValueError):
+                _calls(rt=_routing(0, **{f: bad}))[name]()
+    assert not fake.calls
+    _calls(rt=_routing(0, **{f: 4096 for f in fields}))[name]()  # addresses
+    assert len(fake.calls) == 1
