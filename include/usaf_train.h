@@ -58,7 +58,7 @@ usaf_status usaf_router_aux_fwd(int64_t T, int64_t E, int64_t k, const float* lo
 /* usaf_router_aux_bwd - the gradient of loss[0] with respect to the logits (counts are constants):
  *   dlogit[t,e] = d_loss p[t,e] ( coef_balance E/(k n n[g]) (c[g,e] - sum_j p[t,j] c[g,j])
  *                                 + coef_z 2/n logsumexp(logits[t]) )
- * and 0 for tokens that take no part; p = 0 where a logit is -inf.
+ * and 0 for tokens that take no part and where p = 0 (a logit of -inf), whatever d_loss is.
  *   count, n_tok  as usaf_router_aux_fwd wrote them, or summed over ranks (with one group) for the
  *                 gradient of a whole data-parallel batch's loss
  *   d_loss        [1] fp32 upstream gradient, or NULL for 1

@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(AUX_THREADS, BLOCKS<NV>)
       if (in) {
         float* o = out + tok * ld_out;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[u][i] *= fmaf(cg, c[i] - s, zt);
+        for (int i = 0; i < NV; ++i)  // 0 where p is, whatever the upstream gradient
+          v[u][i] = v[u][i] != 0.f ? v[u][i] * fmaf(cg, c[i] - s, zt) : 0.f;
         if constexpr (VEC) {
 #pragma unroll
           for (int i = 0; i < NV; i += 4) {

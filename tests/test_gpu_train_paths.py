@@ -134,3 +134,32 @@ def test_micro_batches_of_their_own_sequences():
     a, b = whole.g_router.cpu().numpy(), cut.g_router.cpu().numpy()
     assert np.linalg.norm(a) > 0 and rel_l2(b, a) <= 4e-5
     assert cut.aux_count.shape[0] == 2 and int(cut.status.item()) == 0
+
+
+@pytest.mark.parametrize("up", [float("inf"), float("nan")])
+@pytest.mark.parametrize("E", [8, 100])
+def test_tokens_without_a_part_have_no_gradient_under_a_nonfinite_upstream(up, E):
+    """A scaled loss that overflowed: masked tokens, rows without experts, tokens outside the sequences
+    and experts no token may take stay 0 (and what an accumulation held stays there), the rest says so."""
+    dev = device()
+    T, k = 60, 2
+    rng = np.random.default_rng(E)
+    l = to_dev(rng.standard_normal((T, E)).astype(np.float32), dev)
+    l[:, 3] = float("-inf")
+    l[7] = float("-inf")
+    idx = l.topk(k, dim=1).indices.to(torch.int32).reshape(-1)
+    mask = torch.ones(T, dtype=torch.uint8, device=dev)
+    mask[20:30] = 0
+    off = torch.tensor([5, 40, 55], dtype=torch.int32, device=dev)
+    new = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device=dev)
+    cnt, n = new(2, E, dt=torch.int32), new(2, dt=torch.int32)
+    B.router_aux_fwd(l, idx, k, cnt, new(2, E), n, new(3), 1.0, 1.0, token_mask=mask,
+                     group_offset=off)
+    none = torch.zeros(T, E, dtype=torch.bool, device=dev)
+    none[:, 3] = none[7] = none[20:30] = none[:5] = none[55:] = True
+    for acc in (0, 1):
+        st, d = new(1, dt=torch.int32), torch.full((T, E), 0.5, device=dev)
+        B.router_aux_bwd(l, k, cnt, n, d, 1.0, 1.0, d_loss=torch.tensor([up], device=dev),
+                         token_mask=mask, group_offset=off, accumulate=acc, dev_status=st)
+        assert (d[none] == 0.5 * acc).all()
+        assert not torch.isfinite(d[~none]).any() and int(st.item()) == B.DEV_NONFINITE
