@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
   // Every thread waits, the loading ones too: that g_router's kernel has seen the parts written orders
   // nothing for this grid, only that kernel's end does.
   dep_wait();
-  float odd = 0.f;  // NaN once a produced value was not finite
+  bool bad = false;
 
   if (warp == 0) {
     if (lane == 0) {  // ------------------------------------------------ A and B parts
@@ -716,7 +716,8 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
               }
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) odd = fmaf(d[8 * c + j], 0.f, odd);
+            for (int j = 0; j < 8; ++j)  // from there on bf16 rounds to infinity; NaN too
+              bad |= !(fabsf(d[8 * c + j]) < 0x1.FFp127f);
             *at = make_uint4(pack_bf16x2(d[8 * c], d[8 * c + 1]),
                              pack_bf16x2(d[8 * c + 2], d[8 * c + 3]),
                              pack_bf16x2(d[8 * c + 4], d[8 * c + 5]),
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(gx::THREADS, 1)
       __syncwarp();
     }
   }
-  flag_status_warp(p.status, odd != 0.f, USAF_DEV_NONFINITE);
+  flag_status_warp(p.status, bad, USAF_DEV_NONFINITE);
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) flag_status(p.status, USAF_DEV_TIMEOUT);

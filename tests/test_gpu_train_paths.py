@@ -163,3 +163,22 @@ def test_tokens_without_a_part_have_no_gradient_under_a_nonfinite_upstream(up, E
                          token_mask=mask, group_offset=off, accumulate=acc, dev_status=st)
         assert (d[none] == 0.5 * acc).all()
         assert not torch.isfinite(d[~none]).any() and int(st.item()) == B.DEV_NONFINITE
+
+
+def test_dx_that_rounding_makes_infinite_is_reported():
+    """bf16 ends at (2 - 2^-7) 2^127; a finite fp32 sum from half a step above it on rounds to infinity."""
+    dev = device()
+    top = (2 - 2.0 ** -8) * 2.0 ** 127
+    for E in (8, 130):
+        for value, odd in ((np.nextafter(np.float32(top), np.float32(0)), 0),
+                           (np.float32(top), B.DEV_NONFINITE), (-np.float32(top), B.DEV_NONFINITE)):
+            dl = torch.zeros(3, E, device=dev)
+            dl[1, 2] = float(value)
+            w = torch.zeros(E, 64, device=dev)
+            w[2, 9] = 1.0
+            dx = torch.empty(3, 64, dtype=torch.bfloat16, device=dev)
+            st = torch.zeros(1, dtype=torch.int32, device=dev)
+            B.router_grad(dl, None, w, dx=dx, dev_status=st)
+            assert bool(torch.isinf(dx[1, 9])) == bool(odd) and int(st.item()) == odd
+            dx[1, 9] = 0
+            assert not dx.float().any()
