@@ -182,3 +182,27 @@ def test_dx_that_rounding_makes_infinite_is_reported():
             assert bool(torch.isinf(dx[1, 9])) == bool(odd) and int(st.item()) == odd
             dx[1, 9] = 0
             assert not dx.float().any()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_act8_of_very_wide_tokens(bf16):
+    """More feature tiles than a grid's second axis has places: 65,537 of 64."""
+    dev = device()
+    H = 64 * 65536 + 1
+    dt = torch.bfloat16 if bf16 else torch.float32
+    s = B.shape(1, H, 1, 1, 1)
+    cap = B.routed_rows_capacity(s)
+    rt = B.Routing.empty(s, dev)
+    B.route_topk(s, None, None, rt, logits_in=torch.zeros(1, 1, device=dev))
+    x = (torch.arange(H, device=dev) % 127 + 1)[None].to(dt)
+    h = torch.zeros(2, cap, dtype=dt, device=dev)
+    store = B.ActStore8.empty(s, dev)
+    B.act8_save(s, x, h, rt, store)
+    xo, xp = torch.empty_like(x), torch.empty(H, cap, dtype=dt, device=dev)
+    ho, wa = torch.empty_like(h), torch.empty(1, cap, dtype=dt, device=dev)
+    B.act8_restore(s, store, rt, xp, ho, wa, x=xo)
+    torch.cuda.synchronize()
+    row = int((rt.perm_slot[:16] == 0).nonzero()[0, 0])
+    assert torch.equal(xo, x) and torch.equal(xp[:, row], x[0])
+    xp[:, row] = 0
+    assert not xp.any()
