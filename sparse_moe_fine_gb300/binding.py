@@ -214,9 +214,13 @@ class Routing:
                        torch.empty(cap, **i32), torch.empty(cap, **i32), torch.empty(R, **i32))
 
     def c(self) -> _Routing:
-        return _Routing(_ptr(self.topk_idx), _ptr(self.topk_w), _ptr(self.expert_count),
-                        _ptr(self.expert_offset), _ptr(self.perm_tok), _ptr(self.perm_slot),
-                        _ptr(self.slot_row))
+        try:
+            return _Routing(self.topk_idx.data_ptr(), self.topk_w.data_ptr(),
+                            self.expert_count.data_ptr(), self.expert_offset.data_ptr(),
+                            self.perm_tok.data_ptr(), self.perm_slot.data_ptr(),
+                            self.slot_row.data_ptr())
+        except AttributeError:  # a field that is None or an address
+            return _Routing(*[_ptr(getattr(self, f)) for f, _ in _Routing._fields_])
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -573,16 +577,15 @@ def _ok_rows(name, t, dtype, shape, dev):
     return t.data_ptr(), (ld if ld >= n else n)
 
 
-def _buf(name, t, dev, least=1, dtype=None):
-    """The address of a contiguous buffer of at least `least` entries (bytes where no dtype is
-    given); None and bare addresses pass."""
-    if t is None or isinstance(t, int):
+def _buf(name, t, dev, nbytes=1, dtype=None):
+    """The address of a contiguous buffer of at least that many bytes; None and addresses pass."""
+    if t is None or t.__class__ is int:
         return t
-    n = t.numel() * (1 if dtype else t.element_size())
-    if (n < least or t.get_device() != dev or not t.is_contiguous()
+    if (t.nbytes < nbytes or t.get_device() != dev or not t.is_contiguous()
             or (dtype is not None and t.dtype is not dtype)):
-        raise ValueError(f"{name}: expected at least {least} {dtype or 'bytes'}, contiguous, on CUDA "
-                         f"device {dev}, got {list(t.shape)} {t.dtype} on {t.device}")
+        raise ValueError(f"{name}: expected at least {nbytes} contiguous bytes "
+                         f"{'' if dtype is None else f'of {dtype} '}on CUDA device {dev}, got "
+                         f"{list(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
@@ -592,7 +595,7 @@ def _status(t, dev):
 
 def _ws_buf(ws, dev):
     """The address and size in bytes of a workspace."""
-    return _buf("ws", ws, dev), ws.numel() * ws.element_size()
+    return _buf("ws", ws, dev), ws.nbytes
 
 
 def _on(stream, dev):
@@ -725,8 +728,7 @@ def act8_save(s: Shape, x, h, rt: Routing, store: ActStore8, dev_status=None, st
     """usaf_act8_save: x [T,H] and h [2I,R_cap] of a forward into the store."""
     d, sh = x.get_device(), ActStore8.shapes(s)
     xp, hp = _ok("x", x, x.dtype, sh[0], d), _ok("h", h, x.dtype, sh[2], d)
-    _buf("expert_offset", rt.expert_offset, d, s.E + 1, _i32)
-    r = rt.c()
+    r = _Routing(expert_offset=_buf("expert_offset", rt.expert_offset, d, 4 * s.E + 4, _i32))
     _check("usaf_act8_save", lib().usaf_act8_save(
         ctypes.byref(s), _dt(x), xp, hp, ctypes.byref(r), *store.ptrs(sh, d), _status(dev_status, d),
         _on(stream, d)))
@@ -738,10 +740,10 @@ def act8_restore(s: Shape, store: ActStore8, rt: Routing, x_perm, h, wa, x=None,
     d, dt, sh = h.get_device(), h.dtype, ActStore8.shapes(s)
     cap = sh[2][1]
     ptrs = store.ptrs(sh, d)
-    for name, n, kind in (("topk_w", s.T * s.k, _f32), ("expert_offset", s.E + 1, _i32),
-                          ("perm_tok", cap, _i32), ("perm_slot", cap, _i32)):
-        _buf(name, getattr(rt, name), d, n, kind)
-    r = rt.c()
+    r = _Routing(None, _buf("topk_w", rt.topk_w, d, 4 * s.T * s.k, _f32), None,
+                 _buf("expert_offset", rt.expert_offset, d, 4 * s.E + 4, _i32),
+                 _buf("perm_tok", rt.perm_tok, d, 4 * cap, _i32),
+                 _buf("perm_slot", rt.perm_slot, d, 4 * cap, _i32))
     _check("usaf_act8_restore", lib().usaf_act8_restore(
         ctypes.byref(s), _dt(h), *ptrs, ctypes.byref(r), _opt("x", x, dt, sh[0], d),
         _ok("x_perm", x_perm, dt, (s.H, cap), d), _ok("h", h, dt, sh[2], d),
