@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace usaf {
@@ -233,7 +235,9 @@ __device__ __forceinline__ float trunc_rest(float a) {
 // entry of axis i + 1 to the next. Host.
 inline bool map_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* pitch, const uint32_t* box) {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  // threads that come here first at once each look it up, and store the same
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = found.load(std::memory_order_acquire);
   if (!fn) {
     void* ptr = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -242,6 +246,7 @@ inline bool map_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t*
         q != cudaDriverEntryPointSuccess)
       return false;
     fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    found.store(fn, std::memory_order_release);
   }
   cuuint64_t d[4], strides[3];
   cuuint32_t bx[4], es[4] = {1, 1, 1, 1};

@@ -69,3 +69,13 @@ def _in_lambda(text, pos):
         if m.start() < pos < i:
             return True
     return False
+
+
+@pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC)
+                                        if f in SOURCES + ["tc_ptx.cuh", "train.cuh",
+                                                           "abi_train.cu"]))
+def test_functions_keep_no_plain_static_variables(name):
+    """Host threads may call at once, so what a function keeps is atomic (or made of atomics)."""
+    for m in re.finditer(r"^\s+static (?!_|constexpr\b|const\b|assert)([^(;={]*)[;={]", _text(name),
+                         flags=re.M):
+        assert re.match(r"std::atomic<|OncePerDevice\b", m.group(1)), m.group(0)
