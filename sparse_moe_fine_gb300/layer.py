@@ -55,7 +55,33 @@ def allreduce_dense_grad(g_dense, group=None):
     dist.all_reduce(g_dense, op=dist.ReduceOp.SUM, group=group)
 
 
+def _scratch(name):
+    """A buffer of the layer that is allocated when it is first used, so that a layer which is given
+    another's before that (share_activations, share_scratch) never holds one of its own."""
+    def get(self):
+        t = self._held.get(name)
+        if t is None:
+            n, dtype = self._scratch_sizes[name]
+            t = self._held[name] = torch.empty(n, dtype=dtype, device=self.dev)
+            # work of the current stream may still use the memory that the allocator hands out again;
+            # the buffer serves any stream from here on
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(self.dev).synchronize()
+        return t
+
+    def put(self, t):
+        self._held[name] = t
+    return property(get, put)
+
+
 class MoELayer:
+    # what a forward leaves for the backward, outputs, and workspaces
+    x_perm, h, wa, y, dx = (_scratch(n) for n in ("x_perm", "h", "wa", "y", "dx"))
+    ws_route, ws_fwd, ws_bwd = (_scratch(n) for n in ("ws_route", "ws_fwd", "ws_bwd"))
+    ws_rgrad, dlogit_aux = _scratch("ws_rgrad"), _scratch("dlogit_aux")
+    ACTIVATIONS = ("x_perm", "h", "wa")
+    WORKSPACES = ("ws_route", "ws_fwd", "ws_bwd", "ws_rgrad", "dlogit_aux")
+
     def __init__(self, T, H, E, k, I, w_gate_up, w_down, w_router, act_idx, lr=1e-4,
                  betas=(0.9, 0.999), eps=1e-8, renorm=1, device="cuda", group=None,
                  dense_density=0.015, balance_coef=0.0, z_coef=0.0):
@@ -80,11 +106,13 @@ class MoELayer:
         self.rt = B.Routing.empty(self.s, d)
         self.logits = torch.empty(T, E, device=d)
         # per-row activations are feature-major: [features, R_cap]
-        self.x_perm = torch.empty(H, cap, dtype=self.dtype, device=d)
-        self.h = torch.empty(2 * I, cap, dtype=self.dtype, device=d)
-        self.wa = torch.empty(I, cap, dtype=self.dtype, device=d)
-        self.y = torch.empty(T, H, dtype=self.dtype, device=d)
-        self.dx = torch.empty(T, H, dtype=self.dtype, device=d)
+        rows, tokens = lambda n: ((n, cap), self.dtype), ((T, H), self.dtype)
+        bytes_ = lambda n: ((n,), torch.uint8)
+        self._held = {}
+        self._scratch_sizes = {
+            "x_perm": rows(H), "h": rows(2 * I), "wa": rows(I), "y": tokens, "dx": tokens,
+            "ws_route": bytes_(B.route_topk_workspace_size(self.s)),
+            "ws_fwd": bytes_(B.moe_fwd_workspace_size(self.s, self.dt))}
         self.g_router = torch.empty(E, H, device=d)
         # one status word per step parity: the expert update of step i may still be reading its
         # word on the side stream while step i+1 clears and fills the other one
@@ -104,10 +132,6 @@ class MoELayer:
             e.record(self.side)
         self.pending_opt = False
         self.replayed_kernels = 0  # library kernels run by graph replays (graphed_train_step)
-        self.ws_route = torch.empty(B.route_topk_workspace_size(self.s), dtype=torch.uint8,
-                                    device=d)
-        self.ws_fwd = torch.empty(B.moe_fwd_workspace_size(self.s, self.dt), dtype=torch.uint8,
-                                  device=d)
         # auxiliary losses of the router
         self.balance_coef, self.z_coef = float(balance_coef), float(z_coef)
         self.aux = self.balance_coef != 0.0 or self.z_coef != 0.0
@@ -115,9 +139,9 @@ class MoELayer:
         self._shares = {}
         if self.aux:
             self.aux_share()  # made here: a captured step may not allocate it
-            self.dlogit_aux = torch.empty(T, E, device=d)
-            self.ws_rgrad = torch.empty(B.router_grad_workspace_size(T, E, H, self.dtype),
-                                        dtype=torch.uint8, device=d)
+            self._scratch_sizes["dlogit_aux"] = ((T, E), torch.float32)
+            self._scratch_sizes["ws_rgrad"] = bytes_(
+                B.router_grad_workspace_size(T, E, H, self.dtype))
         self.set_sequences()
         # router SparseAdam state (dense over all E*H entries)
         self.r_p = self.w_router.reshape(-1).clone()
@@ -160,8 +184,10 @@ class MoELayer:
         else:
             self.n_dense = 0
         self.g_act = torch.empty(K, device=self.dev)
-        self.ws_bwd = torch.empty(B.moe_bwd_workspace_size(self.s, self.dt, K),
-                                  dtype=torch.uint8, device=self.dev)
+        need = B.moe_bwd_workspace_size(self.s, self.dt, K)
+        self._scratch_sizes["ws_bwd"] = ((need,), torch.uint8)
+        if "ws_bwd" in self._held and self.ws_bwd.numel() < need:
+            del self._held["ws_bwd"]
         self._graphs = {}  # captured steps hold the old active set's pointers
 
     # ------------------------------------------------------------------ auxiliary losses
@@ -258,11 +284,28 @@ class MoELayer:
     def share_activations(self, other):
         """Use another layer's x_perm, h and wa (of the same shape): for layers whose activations
         are kept by save_act8 between their forward and their backward."""
-        mine, theirs = ((L.dtype, L.h.device, L.x_perm.shape, L.h.shape) for L in (self, other))
+        mine, theirs = ([L.dev] + [L._scratch_sizes[n] for n in self.ACTIVATIONS]
+                        for L in (self, other))
         if mine != theirs:
             raise ValueError("layers of different shapes or devices cannot share activation buffers")
-        self.x_perm, self.h, self.wa = other.x_perm, other.h, other.wa
+        for n in self.ACTIVATIONS:
+            self._held[n] = getattr(other, n)
         self._graphs = {}  # captured steps hold the old buffers' pointers
+
+    def share_scratch(self, other):
+        """Use another layer's workspaces where they are as large as this layer's: for layers whose
+        calls follow one another on one stream. Nothing in them outlives a forward or a backward (with
+        the dense expert gradient that follows it)."""
+        for n in self.WORKSPACES:
+            if self.dev == other.dev and n in self._scratch_sizes and \
+                    self._scratch_sizes[n] == other._scratch_sizes.get(n):
+                self._held[n] = getattr(other, n)
+        self._graphs = {}
+
+    def allocate(self):
+        """Allocate the buffers that are not there yet (the first step does it otherwise)."""
+        for n in self._scratch_sizes:
+            getattr(self, n)
 
     # ------------------------------------------------------------------ checkpoint / resume
     def checkpoint(self) -> dict:
@@ -439,6 +482,7 @@ class MoELayer:
 
     def _capture(self, x, dy, par, main):
         status = self.status2[par:par + 1]
+        self.allocate()
         cs = torch.cuda.Stream(device=self.dev)
         cs.wait_stream(main)
         g_route, g_up, g_body = (torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph(),

@@ -42,9 +42,10 @@ class StackTrainer:
                  reselect="rigl", drop_frac=0.3, skip_nonfinite=True, dense_exchange="allreduce",
                  act8=False):
         """act8: keep each layer's activations in 8 bits between its forward and its backward
-        (usaf_act8_save / _restore). Layers of the same shape then share x_perm, h and wa, and all
-        layers two output and two input-gradient buffers per shape, so a layer below the top costs
-        17/16 bytes a value of x and h instead of its own bf16 buffers. The top layer's backward
+        (usaf_act8_save / _restore). Layers of the same shape then share x_perm, h, wa and their
+        workspaces, and all layers two output and two input-gradient buffers per shape, so a layer
+        below the top costs 17/16 bytes a value of x and h instead of its own bf16 buffers (layers
+        allocate those when they first use them: layers that have not run hold none). The top layer's backward
         follows its forward and reads its activations as they are. Layers' y and dx are then only
         what the last call left there.
 
@@ -71,21 +72,23 @@ class StackTrainer:
             self._share_buffers()
 
     def _share_buffers(self):
-        """One x_perm, h, wa and restored input per layer shape, two y and two dx; a store per layer
-        below the top."""
+        """One x_perm, h, wa, set of workspaces and restored input per layer shape, two y and two dx; a
+        store per layer below the top."""
         first, self._x8, flow = {}, {}, {}
-        for i, L in enumerate(self.layers):
-            key = (L.dtype, tuple(L.x_perm.shape), tuple(L.h.shape), L.T)
+        self._key = [(L.dev, L.dtype, L.T, L.H, L.I, B.routed_rows_capacity(L.s))
+                     for L in self.layers]
+        for i, (L, key) in enumerate(zip(self.layers, self._key)):
             if key not in first:
                 first[key] = L
-                self._x8[key] = torch.empty_like(L.y)
+                self._x8[key] = torch.empty(L.T, L.H, dtype=L.dtype, device=L.dev)
             else:
                 L.share_activations(first[key])
-            tokens = (L.dtype, L.T, L.H)
-            ys, dxs = flow.setdefault((tokens, i % 2), (L.y, L.dx))
-            L.y, L.dx = ys, dxs
+                L.share_scratch(first[key])
+            side = (L.dev, L.dtype, L.T, L.H), i % 2
+            if side not in flow:
+                flow[side] = L.y, L.dx
+            L.y, L.dx = flow[side]
             L._graphs = {}
-        self._key = [(L.dtype, tuple(L.x_perm.shape), tuple(L.h.shape), L.T) for L in self.layers]
         self._stores = [B.ActStore8.empty(L.s, L.dev) for L in self.layers[:-1]]
 
     # ------------------------------------------------------------------ one micro-batch

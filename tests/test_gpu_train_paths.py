@@ -206,3 +206,54 @@ def test_act8_of_very_wide_tokens(bf16):
     assert torch.equal(xo, x) and torch.equal(xp[:, row], x[0])
     xp[:, row] = 0
     assert not xp.any()
+
+
+def test_a_stack_of_8_bit_activations_never_holds_all_layers_buffers():
+    """Eight layers, built, stacked and stepped: at no time more than a layer's weights, state, routing
+    tables and store each (10 MB of store, below 8 MB of the rest), and three layers' activations
+    and workspaces (75 MB a layer); eight layers' own would be 600 MB."""
+    dev = device()
+    cfg = synth.small_config("act8_peak", T=4096, H=256, E=4, k=4, I=256, bf16=True, frac=0.05)
+    x = to_dev(synth.moe_inputs(cfg, seed=1)["x"], dev, True)
+    torch.cuda.synchronize()
+    base = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    layers = _layers(dev, cfg, cfg.T, 8, balance_coef=1.0)
+    tr = StackTrainer(layers, total_steps=10, reselect_every=0, act8=True)
+    tr.step([x], [x])
+    torch.cuda.synchronize()
+    peak = torch.cuda.max_memory_allocated() - base
+    own = sum(getattr(layers[0], n).nbytes for n in (
+        "x_perm", "h", "wa", "y", "dx", "ws_route", "ws_fwd", "ws_bwd", "ws_rgrad", "dlogit_aux"))
+    assert own > 70e6 and peak < 8 * 18e6 + 3 * own, (peak, own)
+    assert len({L.ws_bwd.data_ptr() for L in layers}) == 1
+    assert not any(tr.metrics()[0]["skipped"])
+
+
+def test_layers_allocate_when_they_first_run_and_in_a_capture():
+    """A layer holds no buffers before its first step; a step captured before any has run works too."""
+    dev = device()
+    cfg = synth.small_config("lazy", T=256, H=128, E=8, k=2, I=128, bf16=True, frac=0.05)
+    inp = synth.moe_inputs(cfg, seed=2)
+    x, dy = (to_dev(inp[n], dev, True) for n in ("x", "dy"))
+    a, = _layers(dev, cfg, cfg.T, 1)
+    b, = _layers(dev, cfg, cfg.T, 1)
+    assert not a._held and not b._held
+    a.status.zero_()
+    a.route(x)
+    a.forward(x)
+    a.backward(x, dy)
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        b.route(x, s)
+        b.forward(x, s)
+        b.backward(x, dy, stream=s)
+    g.replay()
+    torch.cuda.synchronize()
+    # y and dx are added in any order, the compact gradient is not; rows past the last expert's are
+    # nobody's
+    rows = int(a.rt.expert_offset[-1].item())
+    assert torch.equal(a.g_act, b.g_act) and torch.equal(a.h[:, :rows], b.h[:, :rows])
+    assert rel_l2(b.y.float().cpu().numpy(), a.y.float().cpu().numpy()) <= 1e-2
