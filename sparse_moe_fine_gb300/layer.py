@@ -274,9 +274,10 @@ class MoELayer:
         B.act8_save(self.s, x, self.h, self.rt, store, dev_status=self.status, stream=stream)
         return store
 
-    def restore_act8(self, store, x, stream=None):
+    def restore_act8(self, store, x=None, stream=None):
         """What the backward reads, from the store of this layer's forward: x_perm, h and wa in the
-        layer's buffers, the layer's input in x [T,H]. Returns x."""
+        layer's buffers, the layer's input in x [T,H] (None: not written, for a caller who still has
+        it). Returns x."""
         self._check_tokens(x=x)
         B.act8_restore(self.s, store, self.rt, self.x_perm, self.h, self.wa, x=x, stream=stream)
         return x

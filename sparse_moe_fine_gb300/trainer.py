@@ -78,9 +78,10 @@ class StackTrainer:
         self._key = [(L.dev, L.dtype, L.T, L.H, L.I, B.routed_rows_capacity(L.s))
                      for L in self.layers]
         for i, (L, key) in enumerate(zip(self.layers, self._key)):
+            if 0 < i < len(self.layers) - 1 and key not in self._x8:
+                self._x8[key] = torch.empty(L.T, L.H, dtype=L.dtype, device=L.dev)
             if key not in first:
                 first[key] = L
-                self._x8[key] = torch.empty(L.T, L.H, dtype=L.dtype, device=L.dev)
             else:
                 L.share_activations(first[key])
                 L.share_scratch(first[key])
@@ -108,7 +109,11 @@ class StackTrainer:
             L = self.layers[i]
             x = inputs[i]
             if self.act8 and i < len(self.layers) - 1:
-                x = L.restore_act8(self._stores[i], self._x8[self._key[i]])
+                # the bottom layer's input is the caller's, as it was; the others' went with the next
+                # layer but one
+                x8 = self._x8[self._key[i]] if i > 0 else None
+                restored = L.restore_act8(self._stores[i], x8)
+                x = x if x8 is None else restored
             dx = L.dx if i > 0 else None  # the bottom layer's input needs no gradient
             L.backward_into(x, dy, accumulate=0 if first else 1, dx=dx,
                             aux_share=share(L) if L.aux else None)

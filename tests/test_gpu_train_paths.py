@@ -257,3 +257,20 @@ def test_layers_allocate_when_they_first_run_and_in_a_capture():
     rows = int(a.rt.expert_offset[-1].item())
     assert torch.equal(a.g_act, b.g_act) and torch.equal(a.h[:, :rows], b.h[:, :rows])
     assert rel_l2(b.y.float().cpu().numpy(), a.y.float().cpu().numpy()) <= 1e-2
+
+
+def test_the_bottom_layer_of_an_8_bit_stack_reads_its_own_input():
+    """The bottom layer's input is still the caller's at its backward. With no gradient from above (the
+    layers there have no losses), its router's gradient is dlogit^T x with the exact x, bit for bit
+    that of a stack that keeps everything."""
+    dev = device()
+    x = to_dev(synth.moe_inputs(CFG, seed=5)["x"], dev, True)
+    got = []
+    for act8 in (False, True):
+        layers = _layers(dev, CFG, CFG.T, 1, balance_coef=2.0, z_coef=0.5)
+        layers += _layers(dev, CFG, CFG.T, 2, seed=61)
+        StackTrainer(layers, total_steps=10, reselect_every=0, act8=act8).step(
+            [x], [torch.zeros_like(x)])
+        torch.cuda.synchronize()
+        got.append(layers[0].g_router.clone())
+    assert torch.equal(*got) and got[0].any()
