@@ -14,6 +14,7 @@ from sparse_moe_fine_gb300 import synth
 from sparse_moe_fine_gb300.layer import MoELayer
 from sparse_moe_fine_gb300.trainer import StackTrainer
 
+import test_gpu_train_ops as ops
 from _gpu import device, rel_l2, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -274,3 +275,46 @@ def test_the_bottom_layer_of_an_8_bit_stack_reads_its_own_input():
         torch.cuda.synchronize()
         got.append(layers[0].g_router.clone())
     assert torch.equal(*got) and got[0].any()
+
+
+# Sizes at which the calls take paths of their own, at the bounds of test_gpu_train_ops.py.
+@pytest.mark.parametrize("T,E,k,G", [
+    (8192, 128, 8, 1),        # more chunks than one final block takes: blocks of 32 experts
+    (40000, 128, 8, 50), (40000, 100, 4, 1),    # several rows of a lane in the gradient, groups change
+    (20000, 200, 4, 9), (10000, 500, 3, 7),     # the same with 16 and 32 lanes a row
+    (2600001, 8, 2, 1), (2600001, 8, 2, 5)])    # chunks at their largest
+@pytest.mark.parametrize("mask", ["none", "some"])
+def test_aux_of_long_batches(T, E, k, G, mask):
+    dev = device()
+    l, idx, m, off = ops._aux_inputs(T, E, k, G, T + E, mask, dead=(E - k) // 3)
+    got = ops._aux_run(dev, l, idx, k, G, 1e-2, 1e-3, m, off)
+    ops._aux_check(got, TO.router_aux(l, idx, k, 1e-2, 1e-3, m, off))
+
+
+@pytest.mark.parametrize("T,E,H,bf16", [
+    # g_router's two accumulators of few experts used again and again, the leading one emptied often
+    (8192, 8, 4096, True), (8192, 40, 4096, True), (16383, 128, 2048, True),
+    # dx: several tiles a CTA with each count of boxes and ring slots; one box of features left over
+    (2600, 16, 4160, True), (2600, 17, 4160, True), (2600, 64, 4160, True), (2600, 100, 4160, True),
+    (2600, 150, 4160, True), (2600, 161, 4160, True), (2600, 600, 4160, True),
+    (4000, 200, 1000, False)])
+def test_router_grad_of_long_batches(T, E, H, bf16):
+    dev = device()
+    dl, x, w, g_in, dx_in = ops._grad_inputs(T, E, H, bf16, T + E)
+    d_dl, d_w, d_gi = (to_dev(a, dev) for a in (dl, w, g_in))
+    d_x, d_xi = to_dev(x, dev, bf16), to_dev(dx_in, dev, bf16)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    g, dx = torch.empty(E, H, device=dev), torch.empty_like(d_x)
+    B.router_grad(d_dl, d_x, d_w, g_router=g, g_in=d_gi, dx=dx, dx_in=d_xi, dev_status=st)
+    host = lambda t: t.float().cpu().numpy()
+    ops._grad_check(host(g), host(dx), dl, x, w, g_in, dx_in, bf16)
+    g2, dx2 = torch.empty_like(g), torch.empty_like(dx)  # one product at a time
+    B.router_grad(d_dl, d_x, None, g_router=g2, g_in=d_gi, dev_status=st)
+    B.router_grad(d_dl, None, d_w, dx=dx2, dx_in=d_xi, dev_status=st)
+    assert torch.equal(g2, g) and torch.equal(dx2, dx) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("T,H,E,k,I,bf16", [
+    (3000, 1000, 16, 3, 40, True), (1500, 256, 16, 4, 64, False), (2000, 2048, 32, 4, 128, True)])
+def test_act8_of_larger_layers(T, H, E, k, I, bf16):
+    ops.test_act8_matches_fp64_bit_for_bit(T, H, E, k, I, bf16)
