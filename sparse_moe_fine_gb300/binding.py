@@ -590,12 +590,7 @@ def _buf(name, t, dev, nbytes=1, dtype=None):
 
 
 def _status(t, dev):
-    return _buf("dev_status", t, dev, 4)
-
-
-def _ws_buf(ws, dev):
-    """The address and size in bytes of a workspace."""
-    return _buf("ws", ws, dev), ws.nbytes
+    return None if t is None else _buf("dev_status", t, dev, 4)
 
 
 def _on(stream, dev):
@@ -644,7 +639,7 @@ def router_aux_fwd(logits, topk_idx, k, count, prob_sum, n_tok, loss, coef_balan
         _opt("group_offset", group_offset, _i32, (G + 1,), d), G, float(coef_balance),
         float(coef_z), _ok("count", count, _i32, ge, d), _ok("prob_sum", prob_sum, _f32, ge, d),
         _ok("n_tok", n_tok, _i32, (G,), d), _ok("loss", loss, _f32, (3,), d), _status(dev_status, d),
-        *_ws_buf(ws, d), _on(stream, d)))
+        _buf("ws", ws, d), ws.nbytes, _on(stream, d)))
 
 
 def router_aux_bwd(logits, k, count, n_tok, dlogit, coef_balance, coef_z, d_loss=None,
@@ -689,7 +684,7 @@ def router_grad(dlogit, x, w_router, g_router=None, g_in=None, dx=None, dx_in=No
         T, E, H, _dt(ref), dp, ld, _opt("x", x, dt, th, d),
         _opt("w_router", w_router, _f32, eh, d), _opt("g_in", g_in, _f32, eh, d),
         _opt("g_router", g_router, _f32, eh, d), _opt("dx_in", dx_in, dt, th, d),
-        _opt("dx", dx, dt, th, d), _status(dev_status, d), *_ws_buf(ws, d), _on(stream, d)))
+        _opt("dx", dx, dt, th, d), _status(dev_status, d), _buf("ws", ws, d), ws.nbytes, _on(stream, d)))
 
 
 @dataclass

@@ -597,9 +597,15 @@ __global__ void __launch_bounds__(AUX_THREADS, BLOCKS<NV>)
       const float zt = zc * lse;
       if (in) {
         float* o = out + tok * ld_out;
+        // 0 where p is 0, also under an upstream gradient whose factor is not finite
+        if (fabsf(cg) < 1e28f && fabsf(zt) < 1e38f) {  // counts are below 2^31
 #pragma unroll
-        for (int i = 0; i < NV; ++i)  // 0 where p is, whatever the upstream gradient
-          v[u][i] = v[u][i] != 0.f ? v[u][i] * fmaf(cg, c[i] - s, zt) : 0.f;
+          for (int i = 0; i < NV; ++i) v[u][i] *= fmaf(cg, c[i] - s, zt);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (v[u][i] != 0.f) v[u][i] *= fmaf(cg, c[i] - s, zt);
+        }
         if constexpr (VEC) {
 #pragma unroll
           for (int i = 0; i < NV; i += 4) {

@@ -318,3 +318,19 @@ def test_router_grad_of_long_batches(T, E, H, bf16):
     (3000, 1000, 16, 3, 40, True), (1500, 256, 16, 4, 64, False), (2000, 2048, 32, 4, 128, True)])
 def test_act8_of_larger_layers(T, H, E, k, I, bf16):
     ops.test_act8_matches_fp64_bit_for_bit(T, H, E, k, I, bf16)
+
+
+def test_tokens_without_a_part_have_no_gradient_under_a_huge_upstream():
+    """A finite upstream gradient whose product with the counts is past fp32: 0 stays 0."""
+    dev = device()
+    T, E, k = 200, 64, 4
+    l = torch.randn(T, E, device=dev)
+    l[:, 5] = float("-inf")
+    mask = (torch.arange(T, device=dev) % 3 != 0).to(torch.uint8)
+    idx = l.topk(k, dim=1).indices.to(torch.int32).reshape(-1)
+    new = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device=dev)
+    cnt, n, d = new(1, E, dt=torch.int32), new(1, dt=torch.int32), torch.ones(T, E, device=dev)
+    B.router_aux_fwd(l, idx, k, cnt, new(1, E), n, new(3), 1e4, 1e4, token_mask=mask)
+    B.router_aux_bwd(l, k, cnt, n, d, 1e4, 1e4, d_loss=torch.tensor([3e38], device=dev),
+                     token_mask=mask)
+    assert not d[mask == 0].any() and not d[:, 5].any() and not torch.isfinite(d[mask != 0]).all()
