@@ -269,8 +269,9 @@ class MoELayer:
         and h; x_perm and wa are formed again by restore_act8. x_perm, h and wa may then be
         overwritten until the restore; the routing tables stay as they are."""
         self._check_tokens(x=x)
-        if store is None:
-            store = B.ActStore8.empty(self.s, self.dev)
+        if store is None:  # of the stream that writes it: memory freed there is free there
+            with torch.cuda.stream(self._main(stream)):
+                store = B.ActStore8.empty(self.s, self.dev)
         B.act8_save(self.s, x, self.h, self.rt, store, dev_status=self.status, stream=stream)
         return store
 

@@ -334,3 +334,21 @@ def test_tokens_without_a_part_have_no_gradient_under_a_huge_upstream():
     B.router_aux_bwd(l, k, cnt, n, d, 1e4, 1e4, d_loss=torch.tensor([3e38], device=dev),
                      token_mask=mask)
     assert not d[mask == 0].any() and not d[:, 5].any() and not torch.isfinite(d[mask != 0]).all()
+
+
+def test_a_store_made_for_another_stream_is_that_streams_memory():
+    """A store that save_act8 allocates may be memory that was just freed; it has to have been freed on
+    the stream that writes it, or work pending on the freeing stream would see it overwritten."""
+    dev = device()
+    L, = _layers(dev, CFG, CFG.T, 1)
+    x = to_dev(synth.moe_inputs(CFG, seed=6)["x"], dev, True)
+    L.route(x)
+    L.forward(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    store = L.save_act8(x, stream=side)
+    torch.cuda.synchronize()
+    for t in (store.x_code, store.x_exp, store.h_code, store.h_exp):
+        seg, = [s for s in torch.cuda.memory_snapshot()
+                if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]]
+        assert seg["stream"] == side.cuda_stream
