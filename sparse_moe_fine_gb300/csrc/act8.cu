@@ -454,13 +454,13 @@ __device__ __forceinline__ void gather_bf16(const CUtensorMap& tm, const Act8Arg
 // a time (restore of 4,096 fp32 tokens, 128 experts, top 8, H 2,048: 242 us with one at a time, 176 us so).
 constexpr int XG_ROWS = 128;
 template <typename T>
-__global__ void __launch_bounds__(THREADS)
-    act8_gather_kernel(const Act8Args a, unsigned row_tiles, T* x_perm) {
+__global__ void __launch_bounds__(THREADS) act8_gather_kernel(const Act8Args a, T* x_perm) {
   __shared__ T tile[64][XG_ROWS + 1];
   __shared__ int s_tok[XG_ROWS];  // the rows' tokens, -1 without one
-  // one axis of blocks, rows first: the widest tokens have more tiles than a second axis may
-  const int64_t r0 = (int64_t)(blockIdx.x % row_tiles) * XG_ROWS;
-  const int64_t h0 = (int64_t)(blockIdx.x / row_tiles) * 64;
+  const int64_t r0 = (int64_t)blockIdx.x * XG_ROWS;
+  // the widest tokens have more tiles than the second axis may (one axis and a division: 11% slower)
+  const int64_t h0 = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 64;
+  if (h0 >= a.s.H) return;
   const int64_t end = a.rt.expert_offset[a.s.E], nbx = (a.s.H + BLK - 1) / BLK;
   for (int r = threadIdx.x; r < XG_ROWS; r += THREADS)
     s_tok[r] = r0 + r < end && a.rt.perm_slot[r0 + r] >= 0 ? a.rt.perm_tok[r0 + r] : -1;
@@ -533,10 +533,7 @@ usaf_status restore(const Act8Args& a, void* x_out, void* x_perm, void* h, void*
   g.rows = g.row_segs * ceil_div(a.s.I, ROW_FEATURES);
   g.x = x_out ? ceil_div(a.s.T * a.s.H, X_VECTORS * Vec<T>::N) : 0;
   const int64_t blocks = g.gather + g.rows + g.x;
-  const int64_t row_tiles = a.R_cap / XG_ROWS;
-  const int64_t gather_blocks = tiles ? 0 : row_tiles * ceil_div(a.s.H, 64);
-  if (blocks >= (int64_t(1) << 31) || gather_blocks >= (int64_t(1) << 31))
-    return USAF_ERR_UNSUPPORTED;
+  if (blocks >= (int64_t(1) << 31)) return USAF_ERR_UNSUPPORTED;
   {
     USAF_TRACE("act8_restore", st);
     T *xo = static_cast<T*>(x_out), *ho = static_cast<T*>(h), *wo = static_cast<T*>(wa);
@@ -562,8 +559,10 @@ usaf_status restore(const Act8Args& a, void* x_out, void* x_perm, void* h, void*
   }
   if (tiles) return USAF_OK;
   USAF_TRACE("act8_gather", st);
-  act8_gather_kernel<T><<<(unsigned)gather_blocks, THREADS, 0, st>>>(a, (unsigned)row_tiles,
-                                                                     static_cast<T*>(x_perm));
+  const int64_t wide = ceil_div(a.s.H, 64), most = 32768;
+  const dim3 grid((unsigned)(a.R_cap / XG_ROWS), (unsigned)(wide < most ? wide : most),
+                  (unsigned)ceil_div(wide, most));
+  act8_gather_kernel<T><<<grid, THREADS, 0, st>>>(a, static_cast<T*>(x_perm));
   USAF_CHECK_LAUNCH();
   return USAF_OK;
 }
