@@ -86,7 +86,8 @@ usaf_status usaf_router_aux_bwd(int64_t T, int64_t E, int64_t k, const float* lo
  *   x         needed for g_router;  w_router [E,H] fp32, needed for dx
  *   g_in      [E,H] fp32 or NULL (zero);  g_router [E,H] fp32 out, or NULL to skip; may be g_in
  *   dx_in     [T,H] or NULL (zero);  dx [T,H] out, or NULL to skip; may be dx_in
- *             Neither output may overlap any other input (dx = x is refused).
+ *             Neither output may overlap any other input (dx = x is refused where g_router is
+ *             asked for, whose product reads x).
  *   dev_status gets USAF_DEV_NONFINITE if a produced gradient is NaN/Inf (of bf16 layers an infinite
  *              dlogit or w_router gives NaN), USAF_DEV_TIMEOUT if a tensor-core kernel gave up a wait
  * Sums are fp32, their order is fixed. On tensor cores dlogit and w_router are carried exactly, as

@@ -11,9 +11,12 @@
 // Blocks of 16 with a power of two: on Gaussian values int8 codes are off by 0.73% in norm (0.47%
 // with an exact scale, whose codes and values would have to be rounded twice), 8-bit floats of three
 // mantissa bits by 2.6%. The exponent byte adds 1/16 to the store.
-// Measured (Qwen3-30B-A3B-shaped layer: T 4096, top 8, H 2048, I 768, bf16): save 34 us for 179 MB,
-// restore 74 us for 365 MB, of which 302 MB are written, and writes alone run at 4.0 TB/s on this
-// part (75 us). Mixtral-8x7B-shaped (T 8192, I 14336): both 582 us for 3.69 GB, 93% of the copy rate.
+// Measured (Qwen3-30B-A3B-shaped layer: T 4096, top 8, H 2048, I 768): bf16 save 33 us for 179 MB,
+// restore 73 us for 365 MB, of which 302 MB are written; fp32 save 53 us, restore 176 us (297 and 666
+// MB). Mixtral-8x7B-shaped (T 8192, I 14336, bf16): both 582 us for 3.69 GB, 93% of the copy rate.
+// The small restore is at no rate of the memory (DRAM 58% busy, L2 50%, 1.2 GB of writes go at 4.5 TB/s,
+// its 302 MB at 4.1): its gather blocks come first and wait for the rows they gather, and the blocks
+// that stream come after them.
 #include "tc_ptx.cuh"
 #include "train.cuh"
 
@@ -238,8 +241,9 @@ __device__ __forceinline__ uint4 to_vec(const float (&v)[Vec<T>::N]) {
 }
 
 // silu by exp(-|g|), which does not overflow: far negative gates keep their tiny values. bf16
-// results are rounded to 8 bits, so the fast exponential and quotient (2^-20 and better on the
-// gates that a rounded result can tell apart) serve them.
+// results are rounded to 8 bits (2^-9), so the fast exponential and quotient serve them: the first is
+// documented to 2 + 1.17 |g| units of 2^-23, below 2^-16 for |g| up to 87, where the result leaves
+// fp32's normal numbers; the second to 2 units.
 template <typename T>
 __device__ __forceinline__ float silu_tail(float g) {
   if constexpr (sizeof(T) == 2) {
@@ -374,8 +378,7 @@ __device__ __forceinline__ void restore_x(const Act8Args& a, int64_t blk, T* x) 
 // into the 128-byte swizzled box is free of bank conflicts, and a row's four feature groups are one
 // 32-byte sector of codes. A block keeps its rows' tokens over G_STEPS feature tiles; the copy engine
 // reads a tile while the next one's codes are on their way. H a multiple of 64. 38 us for 134 MiB
-// written (Qwen3-shaped layer), the time that clearing as much memory takes; wider and taller tiles
-// were no faster.
+// written (Qwen3-shaped layer); wider and taller tiles were no faster.
 constexpr int G_ROWS = 256, G_FEATURES = 64, G_STEPS = 4;
 constexpr int G_SMEM = 4 * 8192 + 1024;
 __device__ __forceinline__ void gather_bf16(const CUtensorMap& tm, const Act8Args& a, int rb,

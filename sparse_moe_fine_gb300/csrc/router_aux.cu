@@ -9,8 +9,8 @@
 //
 // A forward reads the logits once (2 MB for 4,096 tokens of 128 experts, 0.3 us of DRAM time), so the
 // calls are bound by launches and by the latency of one round to memory: forward and backward
-// together 13 us for 128 tokens of 8 experts (two launches; the host takes as long to issue them),
-// 16 us for 4,096 of 128 (three), 25 us for 16,383 masked tokens of 128 in 37 packed sequences.
+// together 14 us for 128 tokens of 8 experts (two launches; the host takes as long to issue them),
+// 17 us for 4,096 of 128 (three), 26 us for 16,383 masked tokens of 128 in 37 packed sequences.
 #include <type_traits>
 
 #include "train.cuh"
