@@ -11,7 +11,7 @@ import ctypes
 import functools
 import os
 import re
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -794,6 +794,10 @@ class Gate:
                   int(self.group_top), int(self.renorm), float(self.scale))
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_ref", ctypes.byref(c))
+
+    def __reduce__(self):
+        # copies and pickles are made from the fields: what the library reads is each rule's own
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
 
 
 @functools.lru_cache(maxsize=1024)
