@@ -332,8 +332,9 @@ __device__ __forceinline__ int select_token(const GateParams& p, int64_t t, cons
   // What two entries may be apart and be in the wrong order. Scores are off by less than 2^-22 (softmax: and
   // by NL + 8 roundings of the sum), those formed again by less than half of that; without a bias logits
   // are compared, which are exact; keys are off by their lowest bits. Experts that are all scored again
-  // need not be further apart than those scores are off.
-  constexpr float base = !BIAS ? 0.f : SIG ? 0x1p-20f : 0x1p-19f + (NL + 8) * 0x1p-22f;
+  // need not be further apart than those scores are off. (Logits below the smallest normal number are 2^-149
+  // apart whatever their size, so their keys are off by a number that does not fall with them.)
+  constexpr float base = !BIAS ? (1 << BITS) * 0x1p-147f : SIG ? 0x1p-20f : 0x1p-19f + (NL + 8) * 0x1p-22f;
   const auto margin = [&](float c) { return base + fabsf(c) * ((1 << BITS) * 0x1p-21f); };
   const auto again = [&](float c) { return !BIAS ? 0.f : SIG ? 0x1p-21f + fabsf(c) * 0x1p-22f : margin(c); };
   if (p.G > 1) {
