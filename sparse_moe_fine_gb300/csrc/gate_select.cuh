@@ -393,11 +393,12 @@ __device__ __forceinline__ int select_token(const GateParams& p, int64_t t, cons
     }
     if (p.keep < p.G) {
       // the last group kept and the first that is not: two sums of two scores. (Without a bias scores are off
-      // in proportion, by less than 2^-21 of the largest, and what softmax's sum is off moves all alike.)
+      // in proportion, by less than 2^-21 of the largest, and what softmax's sum is off moves all alike. Only
+      // below 2^-128, where exp(-l) passes fp32, a sigmoid is 0 instead: four are off by less than 2^-125.)
       const float lo = unordered(last), hi = unordered(max(__reduce_max_sync(FULL, left), NOTHING));
       const float size = vx > -INFINITY ? fabsf(vx) + (vy > -INFINITY ? fabsf(vy) : 0.f) : 0.f;
       const float reach =
-          2.f * base +
+          (BIAS ? 2.f * base : 0x1p-125f) +
           __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(size))) * (BIAS ? 0x1p-21f : 0x1p-19f);
       bool unsure = hi > -INFINITY && !none && !(lo - hi > reach);  // the same for all lanes
       // in a row of one logit and one bias throughout all groups are equal, as they are in fp32
