@@ -496,13 +496,20 @@ class MoELayer:
     def optimizer_step(self, stream=None, skip_if_nonfinite=1, router=True):
         """Router update on the calling stream (the next routing reads it; router = False leaves it to
         the caller); expert update on the side stream, which the next forward waits for. A gate's bias
-        moves on the calling stream too."""
+        moves on the calling stream too. With skip_if_nonfinite all of them move or none does."""
         self.step_count += 1
         b1, b2 = self.betas
         main = self._main(stream)
+        balance = self.gate_bias is not None and bool(self.bias_rate)
+        # The backward reports what it finds in its own gradients. Sums over ranks are scanned, both of them
+        # before anything moves: a bias or a router that moved on one rank alone would part the replicas.
+        # (A layer with neither a bias nor a group scans each gradient ahead of its own update.)
+        both = bool(skip_if_nonfinite) and (balance or self.group is not None)
         if self.group is not None:
             with torch.cuda.stream(main):
                 allreduce_grads(self.g_act, self.g_router, self.status, self.group)
+        if both:
+            B.scan_nonfinite(self.g_router.view(-1), self.status, stream=main)
         self.ev_bwd.record(main)
         self.side.wait_event(self.ev_bwd)
         # one scan of the whole gradient, then the update in two parts that only check the status
@@ -520,14 +527,14 @@ class MoELayer:
                                    self.status, stream=self.side)
             ev.record(self.side)
         self.pending_opt = True
-        if skip_if_nonfinite and self.gate_bias is not None and self.bias_rate:
-            main.wait_event(self.ev_scan)  # the bias moves on all ranks or on none
+        if both:
+            main.wait_event(self.ev_scan)
         self.balance_step(main, skip_if_nonfinite)
         if not router:
             return
         B.sparse_adam_step(None, self.g_router, self.r_p, self.r_m, self.r_v, self.w_router,
                            self.E * self.H, None, self.lr, b1, b2, self.eps, self.step_count,
-                           skip_if_nonfinite, self.status, stream=main)
+                           2 if both else skip_if_nonfinite, self.status, stream=main)
 
     def train_step(self, x, dy, stream=None, y=None, dx=None):
         """route -> forward -> sparse backward -> SparseAdam (experts, router). y and dx may name
