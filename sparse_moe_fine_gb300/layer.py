@@ -495,16 +495,18 @@ class MoELayer:
 
     def optimizer_step(self, stream=None, skip_if_nonfinite=1, router=True):
         """Router update on the calling stream (the next routing reads it; router = False leaves it to
-        the caller); expert update on the side stream, which the next forward waits for. A gate's bias
-        moves on the calling stream too. With skip_if_nonfinite all of them move or none does."""
+        the caller, with its gradient scanned); expert update on the side stream, which the next forward
+        waits for. A gate's bias moves on the calling stream too. With skip_if_nonfinite all of them move
+        or none does."""
         self.step_count += 1
         b1, b2 = self.betas
         main = self._main(stream)
         balance = self.gate_bias is not None and bool(self.bias_rate)
         # The backward reports what it finds in its own gradients. Sums over ranks are scanned, both of them
-        # before anything moves: a bias or a router that moved on one rank alone would part the replicas.
-        # (A layer with neither a bias nor a group scans each gradient ahead of its own update.)
-        both = bool(skip_if_nonfinite) and (balance or self.group is not None)
+        # before anything moves: a bias or a router that moved on one rank alone would part the replicas. So is
+        # the gradient of a router that the caller updates, who reads the status word alone. (A layer with
+        # neither a bias nor a group scans each gradient ahead of its own update.)
+        both = bool(skip_if_nonfinite) and (balance or self.group is not None or not router)
         if self.group is not None:
             with torch.cuda.stream(main):
                 allreduce_grads(self.g_act, self.g_router, self.status, self.group)

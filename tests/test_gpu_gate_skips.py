@@ -5,6 +5,8 @@ import torch
 
 from sparse_moe_fine_gb300 import binding as B
 from sparse_moe_fine_gb300 import layer as layer_module
+from sparse_moe_fine_gb300 import synth
+from sparse_moe_fine_gb300.trainer import StackTrainer
 
 from test_gpu_gate_step import CFG, device, make, pytestmark  # noqa: F401
 
@@ -85,3 +87,36 @@ def make_any(dev, seed, rule=dict(score="sigmoid")):
     M = layer_module.MoELayer(CFG.T, CFG.H, CFG.E, CFG.k, CFG.I, L.w_gate_up, L.w_down, L.w_router, L.act,
                               device=dev)
     return M, inp, act, x, dy
+
+
+@pytest.mark.parametrize("opt", [dict(weight_decay=0.1), dict(state_bits=8), dict(max_norm=1.0)],
+                         ids=["fp32", "8bit", "clipped"])
+@pytest.mark.parametrize("total", [router_overflows, experts_overflow, flagged])
+def test_all_routers_stay_when_one_layers_sum_is_not_finite(monkeypatch, opt, total):
+    dev = device()
+    layers = [make(dev, CFG, 50 + i, bias_rate=0.01)[0] for i in range(3)]
+    tr = StackTrainer(layers, total_steps=10, router_adamw=opt)
+    m = synth.moe_inputs(CFG, seed=50)
+    x, dy = (torch.from_numpy(m[n]).to(dev).to(torch.bfloat16) for n in ("x", "dy"))
+    tr.step([x], [dy])
+    routers = lambda: [t.clone() for L in layers for t in (L.r_p, L.w_router)] + [
+        t.view(torch.uint8).clone() for t in tr.router_opt.m + tr.router_opt.v]
+    before, states = routers(), [_trained(L) for L in layers]
+    biases = [L.gate_bias.clone() for L in layers]
+    ranks(monkeypatch, layers, [same, total, same])
+    tr.step([x], [dy])
+    torch.cuda.synchronize()
+    assert _equal(routers(), before)
+    assert _equal(_trained(layers[1]), states[1]) and torch.equal(layers[1].gate_bias, biases[1])
+    for i in (0, 2):                                          # their own step was sound
+        assert not torch.equal(layers[i].p, states[i][2]) and not torch.equal(layers[i].gate_bias, biases[i])
+    ranks(monkeypatch, layers, [same] * 3)
+    tr.step([x], [dy])
+    torch.cuda.synchronize()
+    after = routers()
+    # (the bottom router's; the others' gradients are below 1e-15 here, a step of lr g / eps less than a rounding)
+    assert not torch.equal(after[0], before[0]) and not torch.equal(after[1], before[1])
+    assert all(torch.isfinite(L.r_p).all() for L in layers)
+    skipped = [r["skipped"] for r in tr.metrics()]
+    bad = total is not flagged
+    assert skipped == [[False] * 3, [False, bad, False], [False] * 3]
