@@ -206,6 +206,7 @@ class StackTrainer:
         if self.router_opt is not None:
             self._router_step(lr, status)
         rec = {"step": n, "lr": lr, "status": status, "turnover": None,
+               "router_status": None if self.router_opt is None else self._router_status.clone(),
                "expert_count": [L.rt.expert_count.clone() for L in self.layers],
                "aux_loss": [L.aux_loss.clone() if L.aux else None for L in self.layers]}
         if dense:
@@ -266,7 +267,9 @@ class StackTrainer:
         """Host view of the recorded steps (synchronises): learning rate, whether the step was
         skipped for a non-finite gradient, turnover fraction at reselections, and the load
         balance (largest expert count over the mean) and, where they are on, the auxiliary losses
-        (total, balance, z) of the last micro-batch per layer."""
+        (total, balance, z) of the last micro-batch per layer. router_skipped: whether the step of all
+        routers together (router_adamw; else None) was skipped, for one layer's skip or because the norm
+        of their gradients is not finite, which is known only after the layers' own updates."""
         torch.cuda.synchronize()
         out = []
         for r in self.history:
@@ -276,7 +279,9 @@ class StackTrainer:
                 turnover = [int(t.item()) / L.K for t, L in zip(r["turnover"], self.layers)]
             balance = [float(c.max().item()) / max(1e-9, float(c.float().mean().item()))
                        for c in r["expert_count"]]
+            rs = r["router_status"]
             out.append({"step": r["step"], "lr": r["lr"], "skipped": skipped,
+                        "router_skipped": None if rs is None else bool(int(rs.item()) & 1),
                         "turnover": turnover, "load_balance": balance,
                         "aux_loss": [None if a is None else a.tolist() for a in r["aux_loss"]]})
         return out

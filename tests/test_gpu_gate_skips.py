@@ -1,5 +1,6 @@
-"""Steps that are skipped although every rank's own gradient is finite: the sum over the ranks is not. The sum
-is made in the test, in the place of the ranks' all-reduce. Such a step leaves everything alone."""
+"""Steps that are skipped although every rank's own gradient is finite: the sum over the ranks is not, or only
+the norm of all routers' gradients is not. The sum is made in the test, in the place of the ranks'
+all-reduce. What such a step leaves alone, it leaves alone as a whole, and says so."""
 import pytest
 import torch
 
@@ -120,3 +121,41 @@ def test_all_routers_stay_when_one_layers_sum_is_not_finite(monkeypatch, opt, to
     skipped = [r["skipped"] for r in tr.metrics()]
     bad = total is not flagged
     assert skipped == [[False] * 3, [False, bad, False], [False] * 3]
+
+
+def test_a_skip_of_the_routers_alone_is_recorded(monkeypatch):
+    """A finite gradient whose square passes fp32 is found by the norm, after the layers' own updates."""
+    dev = device()
+    layers = [make(dev, CFG, 60 + i)[0] for i in range(2)]
+    tr = StackTrainer(layers, total_steps=10, router_adamw=dict(max_norm=1.0))
+    m = synth.moe_inputs(CFG, seed=60)
+    x, dy = (torch.from_numpy(m[n]).to(dev).to(torch.bfloat16) for n in ("x", "dy"))
+    tr.step([x], [dy])
+    before, p = [L.r_p.clone() for L in layers], layers[0].p.clone()
+
+    def large(ga, gr, st):
+        gr.view(-1)[5] = 1e30
+    ranks(monkeypatch, layers, [large, same])
+    tr.step([x], [dy])
+    ranks(monkeypatch, layers, [same, same])
+    kept = _equal([L.r_p for L in layers], before)
+    tr.step([x], [dy])
+    got = tr.metrics()
+    assert kept and not torch.equal(layers[0].p, p)
+    assert [r["router_skipped"] for r in got] == [False, True, False]
+    assert [r["skipped"] for r in got] == [[False] * 2] * 3
+    plain = StackTrainer([make(dev, CFG, 62)[0]], total_steps=10)
+    plain.step([x], [dy])
+    assert plain.metrics()[0]["router_skipped"] is None
+
+
+@pytest.mark.parametrize("total", [router_overflows, flagged])
+def test_one_layers_skip_is_one_of_the_routers_too(monkeypatch, total):
+    dev = device()
+    layers = [make(dev, CFG, 64 + i)[0] for i in range(2)]
+    tr = StackTrainer(layers, total_steps=10, router_adamw=dict(weight_decay=0.1))
+    m = synth.moe_inputs(CFG, seed=64)
+    x, dy = (torch.from_numpy(m[n]).to(dev).to(torch.bfloat16) for n in ("x", "dy"))
+    ranks(monkeypatch, layers, [total, same])
+    tr.step([x], [dy])
+    assert tr.metrics()[0]["router_skipped"] is True
