@@ -90,8 +90,8 @@ usaf_status usaf_gate_bwd(int64_t T, int64_t E, int64_t k, const usaf_gate* gate
  * usaf_gate_balance - the step of the balancing bias: with c[e] = sum of count[:,e],
  *   bias[e] += rate * sign(mean(c) - c[e])
  * (experts that got less than their share become easier to choose). Counts are compared exactly.
- *   count [n,E] int32 (expert_count of a step's micro-batches, or the auxiliary losses' counts per
- *         group);  bias [E] fp32, updated
+ *   count [n,E] int32 (expert_count of a step's micro-batches, which has every slot; or the auxiliary
+ *         losses' counts per group, which leave out the tokens that a mask does);  bias [E] fp32, updated
  *   skip_if_nonfinite  1: nothing moves if a bit of USAF_DEV_SKIP_MASK is set in *dev_status when the call
  *         runs, as with a step's other updates; 0: no check
  * Limits: 1 <= E <= 1024, 1 <= n <= 2^20; rate finite. Errors: INVALID_ARG, CUDA.

@@ -23,8 +23,9 @@ Two additions to the step, both off unless asked for (see include/usaf_train.h):
 And another routing rule than softmax top-k (gate, a binding.Gate; see include/usaf_gate.h): scores by
 softmax or sigmoid, experts of the best groups only, scaled weights, and a bias that is added to the
 scores for the choice of experts. The bias is not trained by the gradient: after each step it moves by
-bias_rate toward the experts that got less than their share of the step's tokens. (The auxiliary losses
-are of the logits' softmax whatever the gate's scores.)
+bias_rate toward the experts that got less than their share of the step's tokens, without the padding
+tokens that set_sequences names. (The auxiliary losses are of the logits' softmax whatever the gate's
+scores.)
 """
 from __future__ import annotations
 
@@ -174,8 +175,10 @@ class MoELayer:
                 self.gate_bias = torch.zeros(E, device=d)
                 if gate_bias is not None:
                     self.gate_bias.copy_(gate_bias)
-                # tokens per expert of the step's micro-batches, which move the bias
+                # tokens per expert of the step's micro-batches, which move the bias (slots of weight 0,
+                # where a token had fewer than k experts to take, count like others)
                 self.gate_load = torch.zeros(E, dtype=torch.int32, device=d)
+        self.padded = False  # sequences are given
         self.set_sequences()
         # router SparseAdam state (dense over all E*H entries)
         self.r_p = self.w_router.reshape(-1).clone()
@@ -226,15 +229,16 @@ class MoELayer:
 
     # ------------------------------------------------------------------ auxiliary losses
     def set_sequences(self, group_offset=None, token_mask=None):
-        """The sequences that the auxiliary losses see in the next batches: group_offset [G+1] int32
-        (first token of each packed sequence; None: the batch is one) and token_mask [T] uint8 (0:
-        a padding token that takes no part; None: every token does). The tensors are read by every
-        later step, so a caller that changes only their contents may write into them; they are not
-        part of a checkpoint. With the
-        losses on: aux_count and aux_prob [G,E], aux_n [G] and aux_loss [3] (total, balance, z) hold
+        """The sequences that the auxiliary losses, and the counts that move a gate's bias, see in the
+        next batches: group_offset [G+1] int32 (first token of each packed sequence; None: the batch is
+        one) and token_mask [T] uint8 (0: a padding token that takes no part; None: every token does).
+        The tensors are read by every later step, so a caller that changes only their contents may write
+        into them; they are not part of a checkpoint. With the losses on, or sequences given:
+        aux_count and aux_prob [G,E], aux_n [G] and aux_loss [3] (total, balance, z) hold
         the last forward's values."""
         self._check_sequences(group_offset, token_mask)
-        if not self.aux:
+        was, self.padded = self.padded, group_offset is not None or token_mask is not None
+        if not (self.aux or self.padded or was):
             return
         d, T, E = self.dev, self.T, self.E
         G = 1 if group_offset is None else group_offset.numel() - 1
@@ -248,8 +252,9 @@ class MoELayer:
         self._graphs = {}  # captured steps hold the old buffers' pointers
 
     def _check_sequences(self, group_offset, token_mask):
-        if not self.aux and (group_offset is not None or token_mask is not None):
-            raise ValueError("sequences are only for the auxiliary losses, which are off")
+        if not self.aux and self.gate_bias is None and (group_offset is not None
+                                                        or token_mask is not None):
+            raise ValueError("sequences are only for the auxiliary losses and a gate's bias, which are off")
         for name, t, dt in (("group_offset", group_offset, torch.int32),
                             ("token_mask", token_mask, torch.uint8)):
             if t is None:
@@ -262,6 +267,9 @@ class MoELayer:
             raise ValueError("group_offset needs at least two entries")
 
     def _aux_forward(self, stream=None, dev_status=None):
+        """The losses and the counts of the tokens that take part. (With the losses off only the counts are
+        wanted: a loss that is not finite is then no reason to skip a step.)"""
+        dev_status = dev_status if self.aux else None
         B.router_aux_fwd(self.logits, self.rt.topk_idx, self.k, self.aux_count, self.aux_prob,
                          self.aux_n, self.aux_loss, self.balance_coef, self.z_coef,
                          token_mask=self.token_mask, group_offset=self.group_offset,
@@ -414,7 +422,7 @@ class MoELayer:
     def route(self, x, stream=None):
         self._check_tokens(x=x)
         self._route(x, stream, self.status)
-        if self.aux:
+        if self.aux or self.padded:
             self._aux_forward(stream, self.status)
 
     def _main(self, stream):
@@ -477,10 +485,11 @@ class MoELayer:
         self._router_products(x, dx, self.g_router if accumulate else None, stream, status)
         if self.gate_bias is not None:
             with torch.cuda.stream(self._main(stream)):
+                load = self.aux_count.sum(0, dtype=torch.int32) if self.padded else self.rt.expert_count
                 if accumulate:
-                    self.gate_load.add_(self.rt.expert_count)
+                    self.gate_load.add_(load)
                 else:
-                    self.gate_load.copy_(self.rt.expert_count)
+                    self.gate_load.copy_(load)
 
     def balance_step(self, stream=None, skip_if_nonfinite=0):
         """Moves the balancing bias by the step's counts, of all ranks together; skip_if_nonfinite = 1: not
@@ -602,7 +611,7 @@ class MoELayer:
         with torch.cuda.graph(g_route, stream=cs):
             status.zero_()
             self._route(x, cs, status)
-            if self.aux:
+            if self.aux or self.padded:
                 self._aux_forward(cs, status)
             fwd(B.FWD_GATHER)
         with torch.cuda.graph(g_up, stream=cs):

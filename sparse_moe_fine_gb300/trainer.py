@@ -165,21 +165,22 @@ class StackTrainer:
         to the bottom layer, dy_micro[j] [T,H] the gradient at the top layer's output. The
         layers' gradients are summed over the micro-batches, their auxiliary losses averaged.
         sequences[j]: micro-batch j's (group_offset, token_mask) as MoELayer.set_sequences takes them,
-        for every layer with auxiliary losses (the last one's stay set); a micro-batch then counts by
-        its tokens (data parallel: on every rank or on none). Without it the layers' own sequences hold for every micro-batch, and micro-batches
-        and ranks count alike."""
+        for every layer with auxiliary losses or a gate's bias (the last one's stay set); a micro-batch
+        then counts by its tokens (data parallel: on every rank or on none). Without it the layers' own
+        sequences hold for every micro-batch, and micro-batches and ranks count alike."""
         if len(x_micro) != len(dy_micro) or not x_micro:
             raise ValueError("need the same number (>= 1) of inputs and upstream gradients")
         if sequences is not None:
             if len(sequences) != len(x_micro):
                 raise ValueError("need one (group_offset, token_mask) per micro-batch")
-            if not any(L.aux for L in self.layers):
-                raise ValueError("sequences are only for the auxiliary losses, which are off")
-            for L in self.layers:
+            counting = [L for L in self.layers if L.aux or getattr(L, "gate_bias", None) is not None]
+            if not counting:
+                raise ValueError("sequences are only for the auxiliary losses and a gate's bias, which are off")
+            for L in counting:
                 for s in sequences:
-                    if L.aux:
-                        L._check_sequences(*s)
-            shares = self._shares(sequences)
+                    L._check_sequences(*s)
+            # (shares are of the losses' gradients)
+            shares = self._shares(sequences) if any(L.aux for L in counting) else [None] * len(sequences)
         self.step_no += 1
         n = self.step_no
         lr = cosine_lr(n, self.total_steps, self.lr_peak, self.warmup_steps)
@@ -191,9 +192,8 @@ class StackTrainer:
             share = lambda L: L.aux_share(len(x_micro))
             if sequences is not None:
                 share = lambda L, s=shares[j]: s
-                for L in self.layers:
-                    if L.aux:
-                        L.set_sequences(*sequences[j])
+                for L in counting:
+                    L.set_sequences(*sequences[j])
             inputs = self._forward(x)
             self._backward(inputs, dy, first=(j == 0), dense=dense, share=share)
         status = []
