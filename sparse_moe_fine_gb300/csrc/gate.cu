@@ -135,9 +135,16 @@ __global__ void __launch_bounds__(256) gate_fill_kernel(int64_t T, int E, int k,
   fill_rest(E, o, s_off, tot);
 }
 
-// The same for batches of few chunks, without gate_scan_kernel before it: each block counts all chunks'
-// words itself (up to SCAN_WORDS of them, from L2), `slices` threads an expert.
-constexpr int64_t SCAN_WORDS = 16384;
+// The same for batches of few chunks, without gate_scan_kernel before it: each block counts all chunks' words
+// itself, from L2, `slices` threads an expert. What it reads grows with the square of the chunks, and what a
+// thread reads with chunks * E: it is the faster one up to some 100 chunks, and to 12 to 20 K words (us, without
+// and with the scan; the launch that it saves costs the host some 2 us besides):
+//   E   8:  64 chunks 8.2, 8.3;   128 9.8, 9.2;     160 11.7, 9.3;   512 23.0, 15.2;  2,048 112.6, 48.7
+//   E  64: 128 chunks 9.4, 10.0;  192 13.3, 11.4    E 128: 96 chunks 11.4, 11.5;  128 11.7, 11.7;  192 15.7, 12.9
+//   E 160:  76 chunks 11.6, 11.6; 102 12.8, 11.7    E 256: 64 chunks 12.8, 13.4;  80 15.2, 13.2
+//   E 512:  40 chunks 21.2, 21.3;  64 21.0, 20.3    E 1,024: 24 chunks 43.1, 43.5; 48 43.5, 41.5
+constexpr int64_t FEW_CHUNKS = 128;
+constexpr int64_t FEW_WORDS = 16384;
 __global__ void __launch_bounds__(1024) gate_fill_few_kernel(int64_t T, int E, int k,
                                                              const GateTables o,
                                                              const uint32_t* __restrict__ masks,
@@ -400,7 +407,7 @@ usaf_status gate_topk_launch(const GateArgs& a, const usaf_routing& rt, int64_t 
                        : gate_select_softmax(p, o, w.masks, n, st));
   }
   if (n == 1) return USAF_OK;
-  if (n * a.E <= SCAN_WORDS) {
+  if (n <= FEW_CHUNKS && n * a.E <= FEW_WORDS) {
     USAF_TRACE("gate_fill", st);
     // threads for as many slices as there are chunks, at most 1024
     const int width = (int)round_up(a.E, 32);
