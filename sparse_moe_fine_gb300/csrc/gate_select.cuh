@@ -639,7 +639,12 @@ __global__ void __launch_bounds__(32 * GATE_MAX_WARPS)
   fill_tail(o, s_off[p.E], o.cap, threadIdx.x, blockDim.x);
 }
 
-// The experts a lane holds: as few as will do, so that groups fall on whole lanes where they can.
+// The experts a lane holds: as few as will do of these numbers. A number between two powers of two is worth its
+// code: it sorts and shifts fewer keys, and groups fall on whole lanes where they would not otherwise (16,383
+// tokens, sigmoid with a bias, us; in brackets in 8 groups):
+//   E   96: 3 a lane 20.3 (23.1), 4 a lane 20.8 (32.8)     E 136: 5 a lane 22.0 (35.8),  8 a lane 24.1 (42.8)
+//   E  160: 5 a lane 22.0 (25.6), 8 a lane 23.9 (43.3)     E 192: 6 a lane 22.9 (27.4),  8 a lane 24.0 (43.7)
+//   E  320: 12 a lane 30.5 (56.1), 16 a lane 35.0 (66.9)   E 384: 12 a lane 30.4 (34.3), 16 a lane 35.8 (67.7)
 template <bool SIG, bool BIAS>
 usaf_status select_width(const GateParams& p, const GateTables& o, uint32_t* masks, unsigned blocks,
                          unsigned threads, size_t smem, int tokens, cudaStream_t st) {
@@ -650,9 +655,12 @@ usaf_status select_width(const GateParams& p, const GateTables& o, uint32_t* mas
   const int nl = (p.E + 31) / 32;
   if (nl <= 1) return go(std::integral_constant<int, 1>());
   if (nl <= 2) return go(std::integral_constant<int, 2>());
+  if (nl <= 3) return go(std::integral_constant<int, 3>());
   if (nl <= 4) return go(std::integral_constant<int, 4>());
   if (nl <= 5) return go(std::integral_constant<int, 5>());
+  if (nl <= 6) return go(std::integral_constant<int, 6>());
   if (nl <= 8) return go(std::integral_constant<int, 8>());
+  if (nl <= 12) return go(std::integral_constant<int, 12>());
   if (nl <= 16) return go(std::integral_constant<int, 16>());
   return go(std::integral_constant<int, 32>());
 }

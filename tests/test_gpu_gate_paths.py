@@ -14,3 +14,19 @@ from test_gpu_gate import check, data, device, pytestmark  # noqa: F401
 def test_tables_with_and_without_the_scan(T, E, k):
     l, b = data(T, E, T % 97)
     check(device(), l, k, dict(score="sigmoid"), b)
+
+
+@pytest.mark.parametrize("E,G,Gk", [(65, 5, 2), (96, 8, 3), (96, 1, 1), (93, 3, 2), (129, 3, 1), (160, 32, 9), (161, 7, 2),
+                                    (192, 8, 3), (186, 31, 12), (257, 1, 1), (264, 8, 5), (384, 8, 3), (384, 32, 5),
+                                    (377, 13, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [3, 300])
+def test_experts_a_lane(E, G, Gk, score, T):
+    """Numbers of experts whose lanes hold 3, 5, 6 or 12, with groups of whole lanes and of others."""
+    l, b = data(T, E, E + G, dead=E // 16)
+    l[1] = l[1, 0]                                            # equal logits
+    l[2, ::2] = l[2, 1]
+    rule = dict(score=score, n_group=G, topk_group=Gk, renorm=int(G % 2))
+    k = min(6, E // G * Gk)
+    check(device(), l, k, rule)
+    check(device(), l, k, rule, b)
