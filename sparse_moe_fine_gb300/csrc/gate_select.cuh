@@ -668,13 +668,21 @@ usaf_status select_width(const GateParams& p, const GateTables& o, uint32_t* mas
 template <bool SIG>
 usaf_status select_scores(const GateParams& p, const GateTables& o, uint32_t* masks, int64_t chunks,
                           cudaStream_t st) {
-  // A warp for each token while an SM has no more than 32; from there on several tokens a warp, whose set-up
-  // costs as much as a third of a token: in small blocks at first, so that SMs have much the same number
-  // of tokens (5,001 tokens, 33 an SM: 15.1 us in blocks of 32, 13.6 in blocks of eight), then in whole
-  // chunks. (One chunk alone has the tables to write too. Parts of a chunk without tokens are launched as
+  // A warp for each token, in blocks of whole chunks, while an SM has no more than 32 tokens; from there on four
+  // warps share eight tokens, in blocks small enough that SMs have much the same number of tokens, and for
+  // batches that fill the SMs anyway eight warps share a chunk, which clear and write fewer words. Lanes with
+  // more than 8 experts are slowed by blocks of 1,024 threads at any size. (us by a warp a token, blocks of
+  // eight tokens, chunks of eight warps:)
+  //   E 128:  4,096 tokens 12.4, 12.4, 15.6;  4,864 (32 an SM) 12.6, 13.2, 15.7;  5,001 15.2, 13.4, 15.9;
+  //           9,728 (64 an SM) 18.5, 16.1, 18.0;  16,383 28.0, 21.9, 22.0;  32,768 (216 an SM) 48.7, 37.6, 36.5
+  //   E 256 in 8 groups:  4,864 16.5, 17.2, 20.4;  5,001 19.3, 17.4, 20.7;  16,383 37.0, 28.2, 29.8;
+  //           32,768 64.7, 49.2, 49.7;  65,536 127, 90.4, 89.4
+  //   E 512:  128 tokens 40.1, 36.4, 41.6;  3,000 22.0, 19.0, 22.6;  16,383 52.1, 34.6, 37.3;
+  //           65,536 176, 112.4, 112.4          E 1,024:  4,864 43.7, 44.0, 58.3;  16,383 122, 83.3, 83.5
+  // (One chunk alone has the tables to write too. Parts of a chunk without tokens are launched as
   // well: their bits are zero.)
   const int64_t per_sm = ceil_div(p.T, device_sm_count());
-  const bool small = chunks > 1 && per_sm > 32 && per_sm <= 64;
+  const bool small = chunks > 1 && per_sm <= 128 && (per_sm > 32 || p.E > 256);
   const int tokens = small ? 8 : GATE_CHUNK;
   const unsigned warps = chunks == 1 ? (unsigned)std::max<int64_t>(8, p.T)
                          : small ? 4

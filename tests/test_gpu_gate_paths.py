@@ -30,3 +30,13 @@ def test_experts_a_lane(E, G, Gk, score, T):
     k = min(6, E // G * Gk)
     check(device(), l, k, rule)
     check(device(), l, k, rule, b)
+
+
+@pytest.mark.parametrize("T,E,k", [(4864, 8, 2), (4865, 8, 2),       # 32 tokens an SM of 152, 33
+                                   (19456, 4, 2), (19457, 4, 2),     # 128, 129
+                                   (33, 256, 8), (33, 257, 8), (40, 1024, 8), (1500, 300, 2), (5000, 260, 2)])
+@pytest.mark.parametrize("G", [1, 4])
+def test_blocks_of_chunks_and_of_eight_tokens(T, E, k, G):
+    G = G if E % G == 0 else 1
+    l, b = data(T, E, T % 89)
+    check(device(), l, k, dict(score="sigmoid", n_group=G, topk_group=max(1, G - 1)), b)
