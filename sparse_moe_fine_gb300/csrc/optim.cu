@@ -15,16 +15,28 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int BLOCK8 = USAF_ADAMW_BLOCK;
 constexpr int WARPS = THREADS / 32;
-// Blocks of 128 elements that a warp takes, and groups of four that a thread of the norm takes, by the
-// elements of a list: many for long ones; few for short ones, which have too few for every SM otherwise
-// (860 K elements with 8-bit states: 25 -> 17 us for norm and step; 5 M with fp32 ones: 50 -> 42). 8-bit
-// states need four to have two pairs in flight (28 M elements: 99 us by twos, 84 by eights).
+// Blocks of 128 elements that a warp takes, by the elements of a list: few for short ones, which have too few
+// for every SM otherwise; more for long ones, whose every block looks for its tensor first. 8-bit states need
+// four to have two pairs in flight. (us by 1, 2, 4 and 8 blocks, tensors of equal sizes; in brackets with bf16
+// gradients:)
+//   32 bits, 16 tensors:  256 K elements 3.4, 3.9, 4.9, 6.7;  1 M 6.9, 6.7, 7.0, 9.1;  4 M 20.2, 19.5, 19.8, 21.3;
+//                         8 M 36.9, 36.3, 36.7, 37.6;  128 M 544, 529, 533, 538 (521, 491, 495, 501)
+//           300 tensors:  4.7 M 51, 30, 24, 21;  8.6 M 92, 54, 43, 42;  300 M 2,937, 1,692, 1,251, 1,252
+//   8 bits, 16 tensors:   256 K 3.0, 3.9, 4.9, 6.5 (3.3, 4.4, 5.7, 6.9);  0.5 M 6.7, 6.0, 7.1, 7.5 (6.2, 6.7, 7.4, 7.6);
+//                         1 M 9.0, 7.3, 6.0, 8.2 (7.6, 7.3, 7.3, 10.9);  4 M 28.8, 21.7, 18.5, 17.9 (22.1, 18.1,
+//                         15.9, 16.7);  8 M 54.5, 39.0, 31.5, 30.4 (41.8, 32.1, 27.6, 26.8)
+//           300 tensors:  1.2 M 19, 13, 10, 11;  4.7 M 57, 36, 25, 20;  8.6 M 109, 66, 50, 38
 constexpr int64_t K = 1024;
 int step_per(int64_t n, int bits) {
-  if (n < 4 * K * K) return 1;
-  return bits == 8 ? (n < 16 * K * K ? 4 : 8) : n < 64 * K * K ? 2 : 8;
+  if (n < 512 * K) return 1;
+  if (bits == 32) return n < 8 * K * K ? 2 : 4;
+  return n < 4 * K * K ? 4 : 8;
 }
-int norm_per(int64_t n) { return n < 32 * K * K ? 4 : 16; }
+// Groups of four that a thread of the norm takes (us by 4, 8, 16 and 32; in brackets of bf16 gradients):
+//    16 tensors:  1 M 5.6, 5.3, 6.4, 8.7 (5.3, 4.7, 5.1, 6.5);  2 M 6.0, 6.1, 6.7, 8.9 (6.2, 6.0, 5.8, 6.6);
+//                 8 M 9.8, 9.3, 9.4, 10.3 (8.9, 7.4, 8.5, 8.7);  128 M 80.3, 78.4, 77.5, 77.7 (69.1, 46.9, 44.3, 43.0)
+//   300 tensors:  1.2 M 9.1, 9.5, 9.7, 9.5;  4.7 M 18.4, 14.0, 9.6, 11.7;  8.6 M 29.8, 19.9, 16.8, 15.6
+int norm_per(int64_t n) { return n < 4 * K * K ? 4 : 16; }
 
 struct Desc {
   const void* g;
@@ -679,8 +691,10 @@ __global__ void __launch_bounds__(1024) norm_final_kernel(const float2* __restri
   if (threadIdx.x == 0) finish_norm(sum, max_norm, out, status);
 }
 
-// A few small tensors: all by one block, in one launch, its warps taking 512 elements at a time.
-constexpr int64_t NORM_SMALL = 32768;
+// A few small tensors: all by one block, in one launch, its warps taking 512 elements at a time. (us by one
+// block and by two launches, of which the second costs the host some 2 us besides:  8 K elements 3.1, 3.9;
+// 16 K in 8 tensors 3.5, 3.9;  in 16 3.9, 3.9;  32 K in 8 4.4, 3.8;  in 32 5.9, 4.1;  64 K in 8 6.3, 3.8)
+constexpr int64_t NORM_SMALL = 16384;
 constexpr int NORM_SLICE = 512;
 template <class G>
 __global__ void __launch_bounds__(1024) norm_small_kernel(const __grid_constant__ Table<CAP_SMALL> tab,
@@ -741,7 +755,7 @@ usaf_status in_tables(const usaf_adamw_tensor* t, int64_t count, int per, int64_
   tab.per = per;
   int64_t blocks = 0;
   for (int64_t i = 0; i <= count; ++i) {
-    // (a single tensor has fewer than 2^42 / 8192 blocks: its list is not short)
+    // (a single tensor has fewer than 2^42 / 4096 blocks: its list is not short)
     const int64_t need = i < count ? ceil_div(t[i].n, chunk) : 0;
     if (tab.count && (i == count || tab.count == CAP || blocks + need >= (int64_t(1) << 31))) {
       USAF_TRY(f(tab, (unsigned)blocks));
