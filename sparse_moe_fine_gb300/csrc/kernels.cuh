@@ -16,13 +16,10 @@ struct RouteWs {
   void* wr3;            // [E, 3H] bf16 split of the router weight (tensor-core logits)
 };
 void route_ws_layout(const usaf_moe_shape& s, Carver& c, RouteWs& w);
-// the router logits (*logits: where they are; logits_in if given), and the permutation tables of
-// rt.topk_idx
+// the router logits (*logits: where they are; logits_in if given)
 usaf_status route_logits(const usaf_moe_shape& s, const void* x, usaf_dtype xdt, const float* wr,
                          const float* logits_in, float* logits_out, RouteWs& w,
                          uint32_t* dev_status, const float** logits, cudaStream_t st);
-usaf_status route_permute(const usaf_moe_shape& s, const usaf_routing& rt, RouteWs& w,
-                          cudaStream_t st);
 usaf_status route_launch(const usaf_moe_shape& s, const void* x, usaf_dtype xdt, const float* wr,
                          const float* logits_in, float* logits_out, int renorm,
                          const usaf_routing& rt, RouteWs& w, uint32_t* dev_status,

@@ -298,8 +298,9 @@ usaf_status route_logits(const usaf_moe_shape& s, const void* x, usaf_dtype xdt,
   return USAF_OK;
 }
 
-usaf_status route_permute(const usaf_moe_shape& s, const usaf_routing& rt, RouteWs& w,
-                          cudaStream_t st) {
+// the permutation tables of rt.topk_idx
+static usaf_status route_permute(const usaf_moe_shape& s, const usaf_routing& rt, RouteWs& w,
+                                 cudaStream_t st) {
   const int E = (int)s.E, k = (int)s.k;
   const int64_t R = s.T * s.k;
   USAF_TRACE("route_permute", st);
