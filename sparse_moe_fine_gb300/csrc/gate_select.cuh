@@ -520,7 +520,8 @@ __device__ __forceinline__ int select_token(const GateParams& p, int64_t t, cons
   float a = ok ? my_s : 0.f;
   if (p.renorm) {
     float sum = warp_sum(a);
-    if (!(sum > 0x1p-60f)) {
+    if (__any_sync(FULL, ok && !(a > 0x1p-100f))) {
+      // a score that fp32 has few bits of, or none, while its ratio to the sum may be any number:
       // relative to the largest taken, with s = exp(min(l, 0)) / (1 + exp(-|l|)) or exp(l) / total
       const float pos = SIG ? fminf(my_l, 0.f) : my_l;
       const float top = warp_max(ok ? pos : -INFINITY);

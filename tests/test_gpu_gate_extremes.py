@@ -43,3 +43,17 @@ def test_groups_of_the_smallest_scores(E, G, Gk, renorm):
     l[50:60] += rng.uniform(-16, 4, (10, E)).astype(np.float32)
     rule = dict(score="sigmoid", n_group=G, topk_group=Gk, group_top=2, renorm=renorm)
     check(device(), l, 2, rule)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [8, 64, 160])
+def test_ratios_of_scores_that_are_far_apart(score, E):
+    """Experts taken for their bias: one score is far above the smallest fp32 numbers, another below them, and
+    their ratio is a number like any other."""
+    rng = np.random.default_rng(E)
+    l = rng.uniform(-130, -40, (60, E)).astype(np.float32)
+    l[:, 0] = 3.0                                             # what softmax's scores are relative to
+    l[::3] += 20.0
+    b = np.linspace(8, 9, E, dtype=np.float32)
+    b[0] = -100.0                                             # and no token takes
+    check(device(), l, 4, dict(score=score), b)
