@@ -26,8 +26,8 @@ namespace {
 // in doubles too. With 16,383 tokens of 256 experts in 8 groups some 40 tokens need one of the two. More
 // near experts than lanes go to select_exact, which does the whole token in doubles.
 //
-// What bounds it: instructions (646 a token of 128 experts, 845 of 256 in groups; the integer pipe half
-// busy at 2.5 a clock); a row is read once. 16,383 tokens of 256 experts 22 us, 4,096 of 128 7 us.
+// What bounds it: instructions (646 a token of 128 experts, 910 of 256 in groups; the integer pipe half
+// busy at 2.6 a clock); a row is read once. 16,383 tokens of 256 experts 21 us, 4,096 of 128 7 us.
 // ------------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ float warp_max(float v) {
