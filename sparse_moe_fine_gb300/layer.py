@@ -506,7 +506,7 @@ class MoELayer:
         """Router update on the calling stream (the next routing reads it; router = False leaves it to
         the caller, with its gradient scanned); expert update on the side stream, which the next forward
         waits for. A gate's bias moves on the calling stream too. With skip_if_nonfinite all of them move
-        or none does."""
+        or none does, where the backward or a sum over ranks made a value that is not finite."""
         self.step_count += 1
         b1, b2 = self.betas
         main = self._main(stream)
